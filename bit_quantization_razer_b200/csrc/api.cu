@@ -67,6 +67,7 @@ razer_status run_gemm_w4a4(const uint8_t *codes_a, const uint8_t *scales_a, cons
                            const uint8_t *codes_w, const uint8_t *scales_w, const float *ts_w, razer_format wfmt, int64_t N, int64_t K,
                            void *Y, razer_dtype out_dt, void *workspace, cudaStream_t st);
 size_t gemm_w4a4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+size_t gemm_mx_online_workspace_bytes(int64_t T, int64_t K, int64_t E);
 size_t gemm_variant_workspace_bytes(int64_t M, int64_t N, int64_t K);
 razer_status run_gemm_variant(const void *X, razer_dtype act_dt, int64_t M, const uint8_t *codes, const uint8_t *scales, const float *ts,
                               int block, razer_format sfmt, const VariantV &V, int64_t N, int64_t K, void *Y, razer_dtype out_dt,
@@ -165,6 +166,7 @@ size_t razer_workspace_size(razer_op op, int64_t M_or_B, int64_t N, int64_t K)
     if (op == RAZER_OP_GEMM) return gemm_workspace_bytes(M_or_B, N, K);
     if (op == RAZER_OP_GEMM_W4A4) return M_or_B > 0 && N > 0 && K > 0 ? gemm_w4a4_workspace_bytes(M_or_B, N, K) : 0;
     if (op == RAZER_OP_GEMM_VARIANT) return gemm_variant_workspace_bytes(M_or_B, N, K);
+    if (op == RAZER_OP_GEMM_MX_ONLINE) return gemm_mx_online_workspace_bytes(M_or_B, K, 0);
     return 0;
 }
 

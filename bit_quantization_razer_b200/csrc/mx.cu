@@ -1,0 +1,271 @@
+// MXFP4 quantizer and decoder, and the rearrangement of row-major scale bytes
+// into scale tiles.
+//
+// MXFP4 (OCP Microscaling Formats 1.0, 5.3 and 6.3): blocks of 32 E2M1
+// elements along a row and one E8M0 scale per block.  With m the largest
+// magnitude of a block,
+//   e    = clamp(floor(log2 m) - 2, -127, 127)    (m = 0: -127; 2 = log2 of
+//          E2M1's largest power of two, 4)
+//   code = RN_E2M1(x * 2^-e), ties to the even code, magnitudes above 6 to 6
+//   byte = e + 127; 255 (NaN), with codes of 0, for a block with a NaN or an
+//          infinity.
+// The scale is a power of two, so x * 2^-e is exact in binary32 (a product
+// below its range rounds to code 0 either way) and the hardware E2M1 convert
+// makes the only rounding.
+#include "mx.cuh"
+
+namespace razer {
+namespace mx {
+
+// eight 16-bit inputs in a 16-byte vector
+template <typename T> struct Abs16;
+template <> struct Abs16<__half> {
+    static constexpr unsigned kInf = 0x7C00u;
+    static __device__ __forceinline__ float to_f(unsigned b) { return __half2float(__ushort_as_half((unsigned short)b)); }
+};
+template <> struct Abs16<__nv_bfloat16> {
+    static constexpr unsigned kInf = 0x7F80u;
+    static __device__ __forceinline__ float to_f(unsigned b) { return __uint_as_float(b << 16); }
+};
+
+// four E2M1 codes pairs (8 nibbles, element 0 lowest) of 8 scaled values
+__device__ __forceinline__ unsigned e2m1x8(const float (&v)[8])
+{
+    unsigned r;
+    asm("{ .reg .b8 b0, b1, b2, b3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+        "mov.b32 %0, {b0, b1, b2, b3}; }"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+constexpr int kVecs = 4;            // 16-byte vectors per lane and task
+constexpr int kTaskCols = 256 * kVecs;
+
+// One warp per task of one row x 1024 columns; four lanes share a block of 32
+// (8 elements each: one 16-byte load, one 4-byte store, both contiguous over
+// the warp), two shuffles join the block's largest magnitude.
+template <typename T>
+__global__ void __launch_bounds__(256) quantize_mx_kernel(const T *__restrict__ x, int64_t M, int64_t K, int64_t chunks,
+                                                          const int32_t *__restrict__ offsets, int E, uint8_t *__restrict__ codes,
+                                                          uint8_t *__restrict__ tiles)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+    const int64_t ct = tile_cols(false, K);
+    if (E > 0 && blockIdx.x == 0) check_offsets(offsets, E, (int)M);
+    for (int64_t task = warp; task < M * chunks; task += warps) {
+        const int64_t r = task / chunks;
+        const int64_t c0 = (task - r * chunks) * kTaskCols + 8 * lane;
+        int64_t trow;
+        int in_tile;
+        if (E > 0) {
+            const int e = group_of_row(offsets, E, (int)M, (int)r);
+            if (e < 0) continue;  // behind the last group (or before the first): left as it is
+            const int start = group_edge(offsets, e, (int)M), i = (int)r - start;
+            trow = group_tile_row(start, e) + i / kTileRows;
+            in_tile = i % kTileRows;
+        } else {
+            trow = r / kTileRows;
+            in_tile = (int)(r % kTileRows);
+        }
+        uint8_t *trow_p = tiles + trow * ct * kTileBytes + (in_tile & 31) * 16 + (in_tile >> 5) * 4;
+        uint4 v[kVecs];
+#pragma unroll
+        for (int i = 0; i < kVecs; i++) {
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (c0 + 256 * i < K) v[i] = ldg_stream(x + r * K + c0 + 256 * i);
+        }
+#pragma unroll
+        for (int i = 0; i < kVecs; i++) {
+            if ((task - r * chunks) * kTaskCols + 256 * i >= K) break;  // the same for the whole warp
+            const int64_t c = c0 + 256 * i;
+            unsigned m2 = __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu), __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+            m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
+            m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 2));
+            const unsigned m = max(m2 & 0xFFFFu, m2 >> 16);
+            const unsigned field = __float_as_uint(Abs16<T>::to_f(m)) >> 23;  // binary32 exponent field of the block's largest magnitude
+            const unsigned byte = m >= Abs16<T>::kInf ? 255u : (field > 2u ? field - 2u : 0u);
+            const float inv = __uint_as_float((254u - (byte == 255u ? 0u : byte)) << 23);
+            const float2 a = In16<T>::to_f2(v[i].x), b = In16<T>::to_f2(v[i].y), d = In16<T>::to_f2(v[i].z), f = In16<T>::to_f2(v[i].w);
+            const float s[8] = {a.x * inv, a.y * inv, b.x * inv, b.y * inv, d.x * inv, d.y * inv, f.x * inv, f.y * inv};
+            if (c < K) *reinterpret_cast<unsigned *>(codes + (r * K + c) / 2) = byte == 255u ? 0u : e2m1x8(s);
+            // a word holds the scales of 4 blocks: 16 lanes; blocks past K give 0
+            unsigned w = c < K ? byte << (8 * ((lane >> 2) & 3)) : 0u;
+            w |= __shfl_xor_sync(0xffffffffu, w, 4);
+            w |= __shfl_xor_sync(0xffffffffu, w, 8);
+            if ((lane & 15) == 0 && c < K) *reinterpret_cast<unsigned *>(trow_p + (c / 128) * kTileBytes) = w;
+        }
+    }
+}
+
+// out = code * 2^(byte - 127), exact in binary32, rounded once to the output
+// type; the same tasks as the quantizer
+template <typename TOut>
+__global__ void __launch_bounds__(256) dequant_mx_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ tiles, int64_t M,
+                                                         int64_t K, int64_t chunks, const int32_t *__restrict__ offsets, int E,
+                                                         TOut *__restrict__ out)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+    const int64_t ct = tile_cols(false, K);
+    if (E > 0 && blockIdx.x == 0) check_offsets(offsets, E, (int)M);
+    for (int64_t task = warp; task < M * chunks; task += warps) {
+        const int64_t r = task / chunks;
+        const int64_t c0 = (task - r * chunks) * kTaskCols + 8 * lane;
+        int64_t trow;
+        int in_tile;
+        if (E > 0) {
+            const int e = group_of_row(offsets, E, (int)M, (int)r);
+            if (e < 0) continue;
+            const int start = group_edge(offsets, e, (int)M), i = (int)r - start;
+            trow = group_tile_row(start, e) + i / kTileRows;
+            in_tile = i % kTileRows;
+        } else {
+            trow = r / kTileRows;
+            in_tile = (int)(r % kTileRows);
+        }
+        const uint8_t *trow_p = tiles + trow * ct * kTileBytes + (in_tile & 31) * 16 + (in_tile >> 5) * 4;
+#pragma unroll
+        for (int i = 0; i < kVecs; i++) {
+            const int64_t c = c0 + 256 * i;
+            if (c >= K) break;
+            const unsigned w = __ldg(reinterpret_cast<const unsigned *>(codes + (r * K + c) / 2));
+            const float s = e8m0_value(__ldg(trow_p + (c / 128) * kTileBytes + (c / 32) % 4));
+            unsigned h[4];
+            asm("{ .reg .b8 b0, b1, b2, b3; mov.b32 {b0, b1, b2, b3}, %4;\n"
+                "cvt.rn.f16x2.e2m1x2 %0, b0; cvt.rn.f16x2.e2m1x2 %1, b1; cvt.rn.f16x2.e2m1x2 %2, b2; cvt.rn.f16x2.e2m1x2 %3, b3; }"
+                : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+                : "r"(w));
+            float q[8];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float2 p = In16<__half>::to_f2(h[j]);
+                q[2 * j] = p.x * s;
+                q[2 * j + 1] = p.y * s;
+            }
+            if constexpr (sizeof(TOut) == 4) {
+                float4 *o = reinterpret_cast<float4 *>(out + r * K + c);
+                o[0] = make_float4(q[0], q[1], q[2], q[3]);
+                o[1] = make_float4(q[4], q[5], q[6], q[7]);
+            } else {
+                *reinterpret_cast<uint4 *>(out + r * K + c) = make_uint4(Out16<TOut>::pack(q[0], q[1]), Out16<TOut>::pack(q[2], q[3]),
+                                                                         Out16<TOut>::pack(q[4], q[5]), Out16<TOut>::pack(q[6], q[7]));
+            }
+        }
+    }
+}
+
+// Row-major scale bytes [R, C] -> tiles.  One CTA of 128 threads per tile row
+// and 4 tiles: a thread reads 16 scales of its row, the tiles are put
+// together in shared memory and leave it as whole 512-byte rows.  Rows and
+// columns past the matrix become 0 (a scale of 0 or 2^-127: never a NaN that
+// could meet the zero codes there).  Grouped: the rows of tile row t are
+// those of the group that owns it; tile rows without rows stay as they are.
+__global__ void __launch_bounds__(128) tile_scales_kernel(const uint8_t *__restrict__ rows, int64_t R, int64_t C, int64_t ct, int64_t col_chunks,
+                                                          int64_t trows, const int32_t *__restrict__ offsets, int E, int vec,
+                                                          uint8_t *__restrict__ tiles)
+{
+    __shared__ __align__(16) uint8_t buf[4 * kTileBytes];
+    const int64_t cc = blockIdx.x % col_chunks, tr = blockIdx.x / col_chunks;  // tr counts the tile rows of every batch
+    const int i = threadIdx.x;
+    int64_t row, end;
+    if (E > 0 && blockIdx.x == 0) check_offsets(offsets, E, (int)R);
+    if (E > 0) {
+        // the last group whose first tile row is at most tr
+        int lo = 0, hi = E;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (group_tile_row(group_edge(offsets, mid, (int)R), mid) <= tr) lo = mid;
+            else hi = mid;
+        }
+        const int start = group_edge(offsets, lo, (int)R);
+        const int64_t base = (int64_t)start + (tr - group_tile_row(start, lo)) * kTileRows;
+        end = group_edge(offsets, lo + 1, (int)R);
+        if (base < start || base >= end) return;  // no rows in this tile row (the same for the whole CTA)
+        row = base + i;
+    } else {
+        const int64_t b = tr / trows;
+        row = b * R + (tr - b * trows) * kTileRows + i;
+        end = (b + 1) * R;
+    }
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    const int64_t c0 = cc * 16;
+    if (row < end) {
+        const uint8_t *p = rows + row * C + c0;
+        if (vec && c0 + 16 <= C) {
+            v = *reinterpret_cast<const uint4 *>(p);
+        } else {
+            unsigned w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int j = 0; j < 16; j++)
+                if (c0 + j < C) w[j >> 2] |= (unsigned)p[j] << (8 * (j & 3));
+            v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    const int at = (i & 31) * 16 + (i >> 5) * 4;
+    *reinterpret_cast<unsigned *>(buf + at) = v.x;
+    *reinterpret_cast<unsigned *>(buf + at + kTileBytes) = v.y;
+    *reinterpret_cast<unsigned *>(buf + at + 2 * kTileBytes) = v.z;
+    *reinterpret_cast<unsigned *>(buf + at + 3 * kTileBytes) = v.w;
+    __syncthreads();
+    const int64_t t = cc * 4 + (i >> 5);  // warp w writes tile w
+    if (t < ct) reinterpret_cast<uint4 *>(tiles + (tr * ct + t) * kTileBytes)[i & 31] = reinterpret_cast<const uint4 *>(buf)[i];
+}
+
+static unsigned mx_grid(int64_t warps_wanted)
+{
+    // 8 warps a CTA, at most 8 CTAs an SM
+    int64_t g = (warps_wanted + 7) / 8;
+    const int64_t cap = (int64_t)sm_count() * 8;
+    return (unsigned)(g < 1 ? 1 : (g > cap ? cap : g));
+}
+
+}  // namespace mx
+
+razer_status run_quantize_mx(const void *X, razer_dtype dt, int64_t M, int64_t K, const int32_t *offsets, int E, uint8_t *codes,
+                             uint8_t *tiles, cudaStream_t st)
+{
+    using namespace mx;
+    const int64_t chunks = (K + kTaskCols - 1) / kTaskCols;
+    const unsigned g = mx_grid(M * chunks);
+    if (dt == RAZER_F16)
+        quantize_mx_kernel<__half><<<g, 256, 0, st>>>(reinterpret_cast<const __half *>(X), M, K, chunks, offsets, E, codes, tiles);
+    else
+        quantize_mx_kernel<__nv_bfloat16><<<g, 256, 0, st>>>(reinterpret_cast<const __nv_bfloat16 *>(X), M, K, chunks, offsets, E, codes, tiles);
+    return last_launch_status();
+}
+
+razer_status run_dequant_mx(const uint8_t *codes, const uint8_t *tiles, int64_t M, int64_t K, const int32_t *offsets, int E, void *out,
+                            razer_dtype dt, cudaStream_t st)
+{
+    using namespace mx;
+    const int64_t chunks = (K + kTaskCols - 1) / kTaskCols;
+    const unsigned g = mx_grid(M * chunks);
+    if (dt == RAZER_F32)
+        dequant_mx_kernel<float><<<g, 256, 0, st>>>(codes, tiles, M, K, chunks, offsets, E, reinterpret_cast<float *>(out));
+    else if (dt == RAZER_F16)
+        dequant_mx_kernel<__half><<<g, 256, 0, st>>>(codes, tiles, M, K, chunks, offsets, E, reinterpret_cast<__half *>(out));
+    else
+        dequant_mx_kernel<__nv_bfloat16><<<g, 256, 0, st>>>(codes, tiles, M, K, chunks, offsets, E, reinterpret_cast<__nv_bfloat16 *>(out));
+    return last_launch_status();
+}
+
+razer_status run_tile_scales(const uint8_t *rows, int64_t batch, int64_t R, int64_t C, const int32_t *offsets, int E, uint8_t *tiles,
+                             cudaStream_t st)
+{
+    using namespace mx;
+    const int64_t ct = (C + 3) / 4, col_chunks = (ct + 3) / 4;
+    const int64_t trows = E > 0 ? tile_rows_grouped(R, E) : tile_rows(R);
+    const int vec = (C % 16 == 0 && (reinterpret_cast<uintptr_t>(rows) & 15) == 0) ? 1 : 0;
+    tile_scales_kernel<<<(unsigned)(batch * trows * col_chunks), 128, 0, st>>>(rows, R, C, ct, col_chunks, trows, offsets, E, vec, tiles);
+    return last_launch_status();
+}
+
+}  // namespace razer

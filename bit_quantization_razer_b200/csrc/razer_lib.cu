@@ -11,3 +11,6 @@
 #include "variant_decode.cu"
 #include "gemm.cu"
 #include "gemv_noalloc.cu"
+#include "mx.cu"
+#include "mx_gemm.cu"
+#include "mx_api.cu"

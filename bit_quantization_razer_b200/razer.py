@@ -23,10 +23,12 @@ STATUS_NAMES = {
     7: "RAZER_ERR_TIMEOUT", 8: "RAZER_ERR_CUDA",
 }
 RAZER_F16, RAZER_BF16, RAZER_F32 = 0, 1, 2
-RAZER_FMT_WEIGHT, RAZER_FMT_ACT, RAZER_FMT_NVFP4, RAZER_FMT_FOUR_OVER_SIX, RAZER_SCALE_F16 = 0, 1, 2, 3, 4
-RAZER_OP_GEMV, RAZER_OP_GEMM, RAZER_OP_GEMM_W4A4, RAZER_OP_GEMM_VARIANT = 0, 1, 2, 3
+RAZER_FMT_WEIGHT, RAZER_FMT_ACT, RAZER_FMT_NVFP4, RAZER_FMT_FOUR_OVER_SIX, RAZER_SCALE_F16, RAZER_FMT_MXFP4 = 0, 1, 2, 3, 4, 5
+RAZER_OP_GEMV, RAZER_OP_GEMM, RAZER_OP_GEMM_W4A4, RAZER_OP_GEMM_VARIANT, RAZER_OP_GEMM_MX_ONLINE = 0, 1, 2, 3, 4
+RAZER_ACT_NONE, RAZER_ACT_SILU_MUL = 0, 1
+ACTS = {None: RAZER_ACT_NONE, "silu_mul": RAZER_ACT_SILU_MUL}
 FORMATS = {"weight": RAZER_FMT_WEIGHT, "act": RAZER_FMT_ACT, "nvfp4": RAZER_FMT_NVFP4, "four_over_six": RAZER_FMT_FOUR_OVER_SIX,
-           "f16_scale": RAZER_SCALE_F16}
+           "f16_scale": RAZER_SCALE_F16, "mxfp4": RAZER_FMT_MXFP4}
 _DT = {torch.float16: RAZER_F16, torch.bfloat16: RAZER_BF16, torch.float32: RAZER_F32}
 
 EXPORTED = (
@@ -35,6 +37,8 @@ EXPORTED = (
     "razer_quantize_variant", "razer_quant_error_variant", "razer_dequant_variant", "razer_gemv_variant", "razer_gemm_variant",
     "razer_workspace_size", "razer_get_device_status", "razer_status_string", "razer_version",
     "razer_gemv_noalloc", "razer_gemv_noalloc_max_scratch", "razer_debug_set_fault_injection", "razer_set_quantize_path",
+    "razer_scale_tiles_size", "razer_quantize_mx", "razer_dequant_mx", "razer_tile_scales", "razer_gemm_mx", "razer_gemm_mx_grouped",
+    "razer_gemm_mx_online", "razer_gemm_mx_grouped_online", "razer_gemm_mx_grouped_workspace_size",
 )
 
 
@@ -96,7 +100,19 @@ def load() -> ctypes.CDLL:
     L.razer_debug_set_fault_injection.restype = ctypes.c_int
     L.razer_set_quantize_path.argtypes = [i32]
     L.razer_set_quantize_path.restype = ctypes.c_int
-    for fn in ("razer_quantize_variant", "razer_quant_error_variant", "razer_dequant_variant", "razer_gemv_variant", "razer_gemm_variant",
+    L.razer_scale_tiles_size.argtypes = [i32, i64, i64, i64]
+    L.razer_scale_tiles_size.restype = sz
+    L.razer_quantize_mx.argtypes = [vp, i32, i64, i64, vp, i64, vp, vp, vp]
+    L.razer_dequant_mx.argtypes = [vp, vp, i64, i64, vp, i64, vp, i32, vp]
+    L.razer_tile_scales.argtypes = [vp, i64, i64, i64, vp, i64, vp, vp]
+    L.razer_gemm_mx.argtypes = [vp, vp, vp, i64, vp, vp, vp, i32, i64, i64, i32, vp, i32, vp]
+    L.razer_gemm_mx_grouped.argtypes = [vp, vp, vp, i64, vp, i64, vp, vp, vp, i32, i64, i64, i32, vp, i32, vp]
+    L.razer_gemm_mx_online.argtypes = [vp, i32, i64, vp, vp, i64, i64, i32, vp, i32, vp, sz, vp]
+    L.razer_gemm_mx_grouped_online.argtypes = [vp, i32, i64, vp, i64, vp, vp, i64, i64, i32, vp, i32, vp, sz, vp]
+    L.razer_gemm_mx_grouped_workspace_size.argtypes = [i64, i64, i64]
+    L.razer_gemm_mx_grouped_workspace_size.restype = sz
+    for fn in ("razer_quantize_mx", "razer_dequant_mx", "razer_tile_scales", "razer_gemm_mx", "razer_gemm_mx_grouped",
+               "razer_gemm_mx_online", "razer_gemm_mx_grouped_online", "razer_quantize_variant", "razer_quant_error_variant", "razer_dequant_variant", "razer_gemv_variant", "razer_gemm_variant",
                "razer_gemm_w4a4_online", "razer_quant_error", "razer_gemm_w4a4", "razer_gemv_batch", "razer_quantize_weights", "razer_quantize_weights_batch", "razer_quantize_acts", "razer_dequant", "razer_gemv", "razer_gemm",
                "razer_get_device_status", "razer_version"):
         getattr(L, fn).restype = ctypes.c_int
@@ -376,6 +392,200 @@ def razer_gemm(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, ts: t
                            _DT.get(out.dtype, -1), _p(workspace), wsb, _stream(stream))
     _check("razer_gemm", st)
     return out
+
+
+# ---- microscaled 4-bit operands (MXFP4, NVFP4) on the block-scaled tensor cores ----
+# Scale tiles are uint8 tensors [..., tile rows, tile columns, 512]; include/razer.h
+# gives their layout and that of row groups.
+
+def _mx_shape(fn: str, name: str, t, shape, dtype, dev):
+    """t is a contiguous tensor of this shape, type and device (the library sees only its address)."""
+    if t is None or tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        got = "None" if t is None else f"{tuple(t.shape)} {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}"
+        raise ValueError(f"{fn}: {name} must be a contiguous {tuple(shape)} {dtype} tensor on {dev}, got {got}")
+    return t
+
+
+def _mx_call(fn: str, dev, stream, *args):
+    """Calls the library with dev current and, without a stream, on dev's current stream."""
+    call = getattr(load(), fn)
+    if dev.index == torch.cuda.current_device():
+        _check(fn, call(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, call(*args, _stream(stream)))
+
+
+def _mx_ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _mx_matrix(fn: str, name: str, x, dims: int = 2):
+    if x.dim() != dims or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous {dims}-dimensional CUDA tensor, got {tuple(x.shape)} on {x.device}"
+                         f"{'' if x.is_contiguous() else ', not contiguous'}")
+    return x.shape
+
+
+def _mx_groups(fn: str, offsets, dev) -> int:
+    """Number of row groups (0: none given)."""
+    if offsets is None:
+        return 0
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError(f"{fn}: offsets must hold one entry more than there are groups, and a group at least")
+    _mx_shape(fn, "offsets", offsets, offsets.shape, torch.int32, dev)
+    return offsets.shape[0] - 1
+
+
+def razer_scale_tiles_shape(R: int, K: int, fmt="mxfp4", groups: int = 0) -> tuple[int, int, int]:
+    """Shape of the scale tiles of [R, K] codes, or of R rows in `groups` row groups."""
+    per = 4 * (16 if _fmt(fmt) == RAZER_FMT_NVFP4 else 32)
+    return (R // 128 + groups if groups else -(-R // 128), -(-K // per), 512)
+
+
+def razer_quantize_mx(X: torch.Tensor, offsets: torch.Tensor | None = None, *, codes=None, scales=None, stream=None):
+    """Quantize X [M, K] (fp16/bf16, weights or activations) to MXFP4.  Returns
+    (codes [M, K/2] u8, scale tiles u8).  offsets (int32 [E + 1], device): rows
+    in E groups, as razer_gemm_mx_grouped takes them; rows of no group are left out."""
+    fn = "razer_quantize_mx"
+    M, K = _mx_matrix(fn, "X", X)
+    dev = X.device
+    E = _mx_groups(fn, offsets, dev)
+    shape = razer_scale_tiles_shape(M, K, "mxfp4", E)
+    codes = torch.empty((M, K // 2), dtype=torch.uint8, device=dev) if codes is None else _mx_shape(fn, "codes", codes, (M, K // 2), torch.uint8, dev)
+    scales = torch.empty(shape, dtype=torch.uint8, device=dev) if scales is None else _mx_shape(fn, "scales", scales, shape, torch.uint8, dev)
+    _mx_call(fn, dev, stream, X.data_ptr(), _DT.get(X.dtype, -1), M, K, _mx_ptr(offsets), E, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def razer_dequant_mx(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torch.float32, offsets: torch.Tensor | None = None, *,
+                     out=None, stream=None):
+    """Decode MXFP4 codes [M, K/2] with their scale tiles to [M, K] (one rounding to out_dtype)."""
+    fn = "razer_dequant_mx"
+    M, K2 = _mx_matrix(fn, "codes", codes)
+    dev, K = codes.device, 2 * K2
+    E = _mx_groups(fn, offsets, dev)
+    _mx_shape(fn, "codes", codes, (M, K2), torch.uint8, dev)
+    _mx_shape(fn, "scales", scales, razer_scale_tiles_shape(M, K, "mxfp4", E), torch.uint8, dev)
+    out = torch.empty((M, K), dtype=out_dtype, device=dev) if out is None else _mx_shape(fn, "out", out, (M, K), out_dtype, dev)
+    _mx_call(fn, dev, stream, codes.data_ptr(), scales.data_ptr(), M, K, _mx_ptr(offsets), E, out.data_ptr(), _DT.get(out.dtype, -1))
+    return out
+
+
+def razer_tile_scales(scales: torch.Tensor, offsets: torch.Tensor | None = None, *, out=None, stream=None):
+    """Row-major scale bytes [R, C] or [B, R, C] (as the NVFP4 quantizers write
+    them) to scale tiles [..., tile rows, ceil(C/4), 512]; offsets: R rows in groups."""
+    fn = "razer_tile_scales"
+    if scales.dim() == 3 and offsets is not None:
+        raise ValueError(f"{fn}: row groups need [R, C] scales")
+    shape = _mx_matrix(fn, "scales", scales, 3 if scales.dim() == 3 else 2)
+    dev = scales.device
+    _mx_shape(fn, "scales", scales, shape, torch.uint8, dev)
+    E = _mx_groups(fn, offsets, dev)
+    R, C = shape[-2:]
+    tiles = (*shape[:-2], R // 128 + E if E else -(-R // 128), -(-C // 4), 512)
+    out = torch.empty(tiles, dtype=torch.uint8, device=dev) if out is None else _mx_shape(fn, "out", out, tiles, torch.uint8, dev)
+    _mx_call(fn, dev, stream, scales.data_ptr(), shape[0] if len(shape) == 3 else 1, R, C, _mx_ptr(offsets), E, out.data_ptr())
+    return out
+
+
+def _mx_act(fn: str, act) -> int:
+    if act not in ACTS:
+        raise ValueError(f"{fn}: unknown act {act!r}")
+    return ACTS[act]
+
+
+def _mx_weights(fn: str, codes_w, scales_w, E: int, K: int, fmt, dev, ts_w=None) -> int:
+    """Checks packed weights [N, K/2], or [E, N, K/2] for row groups; returns N."""
+    lead = (E,) if E else ()
+    if codes_w.dim() != 2 + len(lead):
+        raise ValueError(f"{fn}: codes_w must be {'[E, N, K/2]' if E else '[N, K/2]'}, got {tuple(codes_w.shape)}")
+    N = codes_w.shape[-2]
+    _mx_shape(fn, "codes_w", codes_w, (*lead, N, K // 2), torch.uint8, dev)
+    _mx_shape(fn, "scales_w", scales_w, (*lead, *razer_scale_tiles_shape(N, K, fmt)), torch.uint8, dev)
+    if ts_w is not None:
+        _mx_shape(fn, "ts_w", ts_w, (E or 1,), torch.float32, dev)
+    return N
+
+
+def _mx_out(fn: str, out, rows: int, N: int, act: int, out_dtype, dev, make=torch.empty):
+    shape = (rows, N // 2 if act else N)
+    if out is None:
+        return make(shape, dtype=out_dtype, device=dev)
+    return _mx_shape(fn, "out", out, shape, out.dtype, dev)
+
+
+def _mx_product(fn, codes_a, scales_a, offsets, codes_w, scales_w, fmt, out_dtype, ts_a, ts_w, act, out, stream):
+    T, K2 = _mx_matrix(fn, "codes_a", codes_a)
+    dev, K = codes_a.device, 2 * K2
+    E, f, a = _mx_groups(fn, offsets, dev), _fmt(fmt), _mx_act(fn, act)
+    _mx_shape(fn, "codes_a", codes_a, (T, K2), torch.uint8, dev)
+    _mx_shape(fn, "scales_a", scales_a, razer_scale_tiles_shape(T, K, f, E), torch.uint8, dev)
+    if ts_a is not None:
+        _mx_shape(fn, "ts_a", ts_a, (1,), torch.float32, dev)
+    N = _mx_weights(fn, codes_w, scales_w, E, K, f, dev, ts_w)
+    out = _mx_out(fn, out, T, N, a, out_dtype, dev, torch.zeros if E else torch.empty)
+    rows = (codes_a.data_ptr(), scales_a.data_ptr(), _mx_ptr(ts_a), T)
+    _mx_call(fn, dev, stream, *rows, *((offsets.data_ptr(), E) if E else ()), codes_w.data_ptr(), scales_w.data_ptr(), _mx_ptr(ts_w), f, N, K,
+             a, out.data_ptr(), _DT.get(out.dtype, -1))
+    return out
+
+
+def razer_gemm_mx(codes_a: torch.Tensor, scales_a: torch.Tensor, codes_w: torch.Tensor, scales_w: torch.Tensor, fmt="mxfp4",
+                  out_dtype=torch.bfloat16, *, ts_a=None, ts_w=None, act=None, out=None, stream=None):
+    """Y [M, N] = ts_a * ts_w * deq(A [M, K]) . deq(W [N, K])^T of packed operands
+    (codes and scale tiles; fmt "mxfp4" or "nvfp4") on the block-scaled tensor
+    cores.  act="silu_mul": W's rows alternate gate and up, Y [M, N/2]."""
+    return _mx_product("razer_gemm_mx", codes_a, scales_a, None, codes_w, scales_w, fmt, out_dtype, ts_a, ts_w, act, out, stream)
+
+
+def razer_gemm_mx_grouped(codes_a: torch.Tensor, scales_a: torch.Tensor, offsets: torch.Tensor, codes_w: torch.Tensor,
+                          scales_w: torch.Tensor, fmt="mxfp4", out_dtype=torch.bfloat16, *, ts_a=None, ts_w=None, act=None, out=None,
+                          stream=None):
+    """razer_gemm_mx with a weight matrix per row group: rows offsets[e] ..
+    offsets[e+1] - 1 of A [T, K] times W[e] of [E, N, K] (ts_w: [E]).  Rows of
+    no group are not written (zeros, where the output is made here)."""
+    if offsets is None:
+        raise ValueError("razer_gemm_mx_grouped: offsets are needed")
+    return _mx_product("razer_gemm_mx_grouped", codes_a, scales_a, offsets, codes_w, scales_w, fmt, out_dtype, ts_a, ts_w, act, out, stream)
+
+
+def _mx_online(fn, X, offsets, codes_w, scales_w, out_dtype, act, out, workspace, stream):
+    T, K = _mx_matrix(fn, "X", X)
+    dev = X.device
+    E, a = _mx_groups(fn, offsets, dev), _mx_act(fn, act)
+    N = _mx_weights(fn, codes_w, scales_w, E, K, RAZER_FMT_MXFP4, dev)
+    out = _mx_out(fn, out, T, N, a, out_dtype, dev, torch.zeros if E else torch.empty)
+    L = load()
+    need = L.razer_gemm_mx_grouped_workspace_size(T, K, E) if E else L.razer_workspace_size(RAZER_OP_GEMM_MX_ONLINE, T, N, K)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be a contiguous tensor on {dev}")
+    _mx_call(fn, dev, stream, X.data_ptr(), _DT.get(X.dtype, -1), T, *((offsets.data_ptr(), E) if E else ()), codes_w.data_ptr(),
+             scales_w.data_ptr(), N, K, a, out.data_ptr(), _DT.get(out.dtype, -1), workspace.data_ptr(),
+             workspace.numel() * workspace.element_size())
+    return out
+
+
+def razer_gemm_mx_online(X: torch.Tensor, codes_w: torch.Tensor, scales_w: torch.Tensor, out_dtype=torch.bfloat16, *, act=None, out=None,
+                         workspace=None, stream=None):
+    """Quantize X [M, K] (fp16/bf16) to MXFP4 and multiply it with MXFP4 weights
+    in one call; equals razer_quantize_mx followed by razer_gemm_mx."""
+    return _mx_online("razer_gemm_mx_online", X, None, codes_w, scales_w, out_dtype, act, out, workspace, stream)
+
+
+def razer_gemm_mx_grouped_online(X: torch.Tensor, offsets: torch.Tensor, codes_w: torch.Tensor, scales_w: torch.Tensor,
+                                 out_dtype=torch.bfloat16, *, act=None, out=None, workspace=None, stream=None):
+    """razer_quantize_mx and razer_gemm_mx_grouped in one call, X [T, K] (fp16/bf16)."""
+    if offsets is None:
+        raise ValueError("razer_gemm_mx_grouped_online: offsets are needed")
+    return _mx_online("razer_gemm_mx_grouped_online", X, offsets, codes_w, scales_w, out_dtype, act, out, workspace, stream)
+
+
+def razer_gemm_mx_grouped_workspace_size(T: int, K: int, groups: int) -> int:
+    """Workspace bytes of razer_gemm_mx_grouped_online."""
+    return int(load().razer_gemm_mx_grouped_workspace_size(T, K, groups))
 
 
 def razer_get_device_status(stream=None) -> int:

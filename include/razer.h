@@ -89,10 +89,20 @@ typedef enum {
      * scale of the pages' kernel format (RaZeR notes, 关键设计 3) -- a 16-bit
      * scale word per block, s = RN_fp16(amax_b / 6) in bits 13..0 (saturating
      * at 0x3FFF), the meta in bits 15..14, no tensor scale (ts = 1). */
-    RAZER_SCALE_F16 = 4
+    RAZER_SCALE_F16 = 4,
+    /* the razer_..._mx calls only: MXFP4 of the OCP Microscaling Formats 1.0
+     * -- blocks of 32 E2M1 codes, one E8M0 scale byte (2^(byte - 127), 255 is
+     * NaN) per block, no tensor scale; 0b1000 means -0. */
+    RAZER_FMT_MXFP4 = 5
 } razer_format;
 
-typedef enum { RAZER_OP_GEMV = 0, RAZER_OP_GEMM = 1, RAZER_OP_GEMM_W4A4 = 2, RAZER_OP_GEMM_VARIANT = 3 } razer_op;
+typedef enum {
+    RAZER_OP_GEMV = 0,
+    RAZER_OP_GEMM = 1,
+    RAZER_OP_GEMM_W4A4 = 2,
+    RAZER_OP_GEMM_VARIANT = 3,
+    RAZER_OP_GEMM_MX_ONLINE = 4
+} razer_op;
 
 /*
  * razer_quantize_weights -- offline weight quantizer (RaZeR notes, 关键设计
@@ -433,17 +443,141 @@ razer_status razer_gemv_noalloc(const void *x, razer_dtype act_dt, int64_t B, co
 /* Size in bytes of the fixed scratch array used by razer_gemv_noalloc. */
 size_t razer_gemv_noalloc_max_scratch(void);
 
+/*
+ * Microscaled 4-bit operands on the tensor cores.  razer_gemm_mx and its
+ * relatives give packed MXFP4 or NVFP4 operands to the block-scaled tcgen05
+ * MMA as they are (nothing is decoded); RaZeR's remapped code has no form
+ * there, so RAZER_FMT_WEIGHT / ACT tensors stay with razer_gemm_w4a4.
+ *
+ * Scale tiles.  These calls keep scale bytes in tiles of 128 rows x 4 scales,
+ * 512 bytes each, row-major over the tiles.  Of a [R, K] tensor with C = K /
+ * block scales per row (block 32: MXFP4; 16: NVFP4), the scale of row r and
+ * block c is byte (r % 32) * 16 + (r % 128) / 32 * 4 + c % 4 of tile
+ * (r / 128, c / 4); there are ceil(R / 128) x ceil(C / 4) tiles.  Scales of a
+ * row's last tile that lie past C are 0 (whoever writes tiles must see to
+ * that: they meet zero codes in the MMA, and a NaN there would spread); rows
+ * past R may hold anything.
+ *
+ * Row groups.  The grouped forms (E > 0) take rows sorted by expert: offsets
+ * is a DEVICE array of E + 1 int32, group e has the rows offsets[e] ..
+ * offsets[e + 1] - 1 of the [T, K] matrix, 0 <= offsets[0] <= ... <=
+ * offsets[E] <= T.  Groups may be empty.  Rows before offsets[0] and from
+ * offsets[E] on belong to no group: nothing is read from them and their
+ * outputs stay as they were.  The scales of group e start a tile row of their
+ * own: row r's tile row is offsets[e] / 128 + e + (r - offsets[e]) / 128, its
+ * place in the tile that of row (r - offsets[e]) % 128; T / 128 + E tile rows
+ * hold every group.  The offsets are read on the device, so nothing
+ * synchronises; offsets that break the rules are brought into 0..T (nothing is
+ * read or written out of range), the outputs are then void and
+ * razer_get_device_status reports RAZER_ERR_INVALID_ARG.
+ *
+ * K % 32 == 0 for both formats (rows of codes are whole 16-byte units); an
+ * NVFP4 tensor with another K runs through razer_gemm_w4a4.  Code and scale
+ * tile pointers 16-byte aligned, offsets 4-byte.  E = 0: dense, offsets NULL.
+ */
+
+/* Bytes of the scale tiles of a [R, K] tensor (E = 0) or of R rows in E groups. */
+size_t razer_scale_tiles_size(razer_format fmt, int64_t R, int64_t K, int64_t E);
+
+/*
+ * razer_quantize_mx -- MXFP4 quantizer for weights and activations.  Per block
+ * of 32 with m = max |x|:  e = clamp(floor(log2 m) - 2, -127, 127) (m = 0:
+ * -127), scale byte e + 127, code = the E2M1 value nearest to x * 2^-e, ties
+ * to the even code, magnitudes above 6 to 6.  A block that holds a NaN or an
+ * infinity gets scale byte 255 and codes of 0 (every element decodes to NaN).  Bit-exact
+ * against this definition; a negative x that rounds to 0 is coded 0b1000.
+ *   X            [M, K], in_dt = RAZER_F16 or RAZER_BF16
+ *   codes        [M, K/2] output;  scale_tiles output
+ *   offsets, E   row groups, or NULL and 0
+ */
+razer_status razer_quantize_mx(const void *X, razer_dtype in_dt, int64_t M, int64_t K, const int32_t *offsets,
+                               int64_t E, uint8_t *codes, uint8_t *scale_tiles, razer_stream_t stream);
+
+/*
+ * razer_dequant_mx -- MXFP4 decoder: out[r, k] = round_out(q * 2^(byte - 127)),
+ * exact in binary32, one rounding to out_dt (f16 / bf16 / f32).  out [M, K].
+ */
+razer_status razer_dequant_mx(const uint8_t *codes, const uint8_t *scale_tiles, int64_t M, int64_t K,
+                              const int32_t *offsets, int64_t E, void *out, razer_dtype out_dt, razer_stream_t stream);
+
+/*
+ * razer_tile_scales -- row-major scale bytes, as razer_quantize_weights /
+ * razer_quantize_acts write them for RAZER_FMT_NVFP4 (or as a checkpoint
+ * stores MXFP4's), to scale tiles.
+ *   scales       [batch, R, C] input (any alignment)
+ *   scale_tiles  [batch] tile matrices, or with E > 0 (batch = 1) the tiles of
+ *                R rows in E groups; what pads a tile is written as 0
+ */
+razer_status razer_tile_scales(const uint8_t *scales, int64_t batch, int64_t R, int64_t C, const int32_t *offsets,
+                               int64_t E, uint8_t *scale_tiles, razer_stream_t stream);
+
+/* What a product writes: the sums, or (RAZER_ACT_SILU_MUL) for weights whose
+ * row 2j is a gate and row 2j + 1 its up projection, the N / 2 outputs
+ * Y[m, j] = silu(g) * u = g / (1 + exp(-g)) * u, with g = sum of row 2j and u
+ * = sum of row 2j + 1 in fp32 and one rounding to out_dt. */
+typedef enum { RAZER_ACT_NONE = 0, RAZER_ACT_SILU_MUL = 1 } razer_act;
+
+/*
+ * razer_gemm_mx -- product of two packed operands of one format:
+ *   Y[m, n] = ts_a * ts_w * sum_k (q*s)_a[m, k] * (q*s)_w[n, k],  fp32 accumulation.
+ *   codes_a, scales_a  A [M, K] (codes and scale tiles)
+ *   codes_w, scales_w  W [N, K]
+ *   ts_a, ts_w         device floats: RAZER_FMT_NVFP4 needs both; MXFP4 has no
+ *                      tensor scale, NULL counts as 1
+ *   fmt                RAZER_FMT_MXFP4 or RAZER_FMT_NVFP4
+ *   Y                  [M, N], or [M, N / 2] with RAZER_ACT_SILU_MUL (N even);
+ *                      out_dt = RAZER_F32, RAZER_F16 or RAZER_BF16
+ * Any M, N >= 0, K % 32 == 0 (K = 0: zeros); no workspace.  Deterministic.
+ */
+razer_status razer_gemm_mx(const uint8_t *codes_a, const uint8_t *scales_a, const float *ts_a, int64_t M,
+                           const uint8_t *codes_w, const uint8_t *scales_w, const float *ts_w, razer_format fmt,
+                           int64_t N, int64_t K, razer_act act, void *Y, razer_dtype out_dt, razer_stream_t stream);
+
+/*
+ * razer_gemm_mx_grouped -- the same product with one weight matrix per row
+ * group: Y[t, n] = ts_a * ts_w[e] * sum_k A[t, k] * W[e, n, k] for the rows t
+ * of group e.
+ *   codes_a, scales_a  A [T, K], scale tiles of the row groups
+ *   codes_w            [E, N, K/2];  scales_w [E] tile matrices of [N, K]
+ *   ts_w               device float[E] (or NULL for MXFP4); ts_a one float
+ *   Y                  [T, N] or [T, N / 2]: rows of no group are not written
+ * E >= 1, E * N < 2^31.
+ */
+razer_status razer_gemm_mx_grouped(const uint8_t *codes_a, const uint8_t *scales_a, const float *ts_a, int64_t T,
+                                   const int32_t *offsets, int64_t E, const uint8_t *codes_w,
+                                   const uint8_t *scales_w, const float *ts_w, razer_format fmt, int64_t N, int64_t K,
+                                   razer_act act, void *Y, razer_dtype out_dt, razer_stream_t stream);
+
+/*
+ * razer_gemm_mx_online / razer_gemm_mx_grouped_online -- razer_quantize_mx on
+ * the activations X (fp16 / bf16) and the product with MXFP4 weights in one
+ * call; Y equals that of the two calls.
+ *   workspace  razer_workspace_size(RAZER_OP_GEMM_MX_ONLINE, M, N, K) or
+ *              razer_gemm_mx_grouped_workspace_size(T, K, E) bytes (16-byte
+ *              aligned; contents on entry ignored): the packed activations
+ */
+razer_status razer_gemm_mx_online(const void *X, razer_dtype x_dt, int64_t M, const uint8_t *codes_w,
+                                  const uint8_t *scales_w, int64_t N, int64_t K, razer_act act, void *Y,
+                                  razer_dtype out_dt, void *workspace, size_t ws_bytes, razer_stream_t stream);
+razer_status razer_gemm_mx_grouped_online(const void *X, razer_dtype x_dt, int64_t T, const int32_t *offsets,
+                                          int64_t E, const uint8_t *codes_w, const uint8_t *scales_w, int64_t N,
+                                          int64_t K, razer_act act, void *Y, razer_dtype out_dt, void *workspace,
+                                          size_t ws_bytes, razer_stream_t stream);
+size_t razer_gemm_mx_grouped_workspace_size(int64_t T, int64_t K, int64_t E);
+
 /* Bytes of workspace razer_gemv (RAZER_OP_GEMV; M_or_B = B), razer_gemm
  * (RAZER_OP_GEMM), razer_gemm_w4a4 / razer_gemm_w4a4_online
- * (RAZER_OP_GEMM_W4A4) and razer_gemm_variant (RAZER_OP_GEMM_VARIANT) need
- * for these sizes (M_or_B = M for the GEMMs); 0 when none. */
+ * (RAZER_OP_GEMM_W4A4), razer_gemm_variant (RAZER_OP_GEMM_VARIANT) and
+ * razer_gemm_mx_online (RAZER_OP_GEMM_MX_ONLINE) need for these sizes (M_or_B
+ * = M for the GEMMs); 0 when none. */
 size_t razer_workspace_size(razer_op op, int64_t M_or_B, int64_t N, int64_t K);
 
 /*
  * razer_get_device_status -- the device-side error word of the current
  * device: RAZER_OK, or RAZER_ERR_TIMEOUT when a bounded wait inside a kernel
  * (pipeline barrier of razer_gemm or of the TMA razer_gemv) gave up.  Synchronises `stream`, then
- * reads and clears the word.
+ * reads and clears the word.  RAZER_ERR_INVALID_ARG: a grouped call read
+ * offsets that break the rules.
  */
 razer_status razer_get_device_status(razer_stream_t stream);
 
