@@ -37,6 +37,7 @@
 
 #include "razer_internal.cuh"
 #include "sm100_async.cuh"
+#include "sm100_mma.cuh"
 #include "variant.cuh"
 
 namespace razer {
@@ -71,22 +72,6 @@ constexpr uint32_t B_BYTES = BN * BK * 2;                            // decoded 
 constexpr uint32_t STAGE_BYTES = kMBlocks * A_HALF_BYTES + B_BYTES;  // 64 KB (256x256) / 80 KB (512x128)
 constexpr uint32_t BAR_BYTES = 256;
 constexpr uint32_t SMEM_BYTES = STAGES * STAGE_BYTES + BAR_BYTES + 1024;  // + alignment slack
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// UMMA shared-memory descriptor of a K-major, 128B-swizzled tile whose
-// 8-row groups are 1024 bytes apart (rows of 128 bytes).
-__device__ __forceinline__ uint64_t smem_desc_k128(uint32_t addr)
-{
-    uint64_t d = 0;
-    d |= (uint64_t)((addr & 0x3FFFFu) >> 4);  // start address
-    d |= (uint64_t)1 << 16;                   // leading byte offset (unused for 128B swizzle)
-    d |= (uint64_t)(1024 >> 4) << 32;         // stride byte offset: 8 rows x 128 B
-    d |= (uint64_t)1 << 46;                   // descriptor version for sm_100
-    d |= (uint64_t)2 << 61;                   // 128-byte swizzle
-    return d;
-}
-
 // kind::f16 instruction descriptor: fp32 accumulate, K-major A and B.
 __host__ __device__ constexpr uint32_t idesc_f16(bool bf16, int M, int N)
 {
@@ -99,27 +84,6 @@ __device__ __forceinline__ void umma_f16(uint32_t dtmem, uint64_t adesc, uint64_
         "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(dtmem), "l"(adesc),
         "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-__device__ __forceinline__ void umma_commit(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
-{
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,"
-        "%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
-          "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
 }
 
 template <int L>
@@ -497,11 +461,6 @@ template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 
     __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(a.z, a.w);
     *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<unsigned *>(&lo), *reinterpret_cast<unsigned *>(&hi));
 }
-template <typename TOut> __device__ __forceinline__ void store1(TOut *p, float a);
-template <> __device__ __forceinline__ void store1<float>(float *p, float a) { *p = a; }
-template <> __device__ __forceinline__ void store1<__half>(__half *p, float a) { *p = __float2half_rn(a); }
-template <> __device__ __forceinline__ void store1<__nv_bfloat16>(__nv_bfloat16 *p, float a) { *p = __float2bfloat16_rn(a); }
-
 // One epilogue warp's row-contiguous write of a staged 32 x 32 chunk whose
 // top-left output element is (m, n): lane l writes 4 elements of row
 // 4 p + l / 8, for p = 0..7.

@@ -17,58 +17,134 @@
 // Every wait is bounded (~2 s of globaltimer): on expiry the kernel records
 // RAZER_ERR_TIMEOUT, the other roles stop at their next wait, copies in
 // flight are waited for (bounded) and the tensor memory is freed.
+#include <algorithm>
+
 #include "mx.cuh"
 #include "sm100_async.cuh"
+#include "sm100_mma.cuh"
 
 namespace razer {
 namespace mx {
 
-using gemm::smem_desc_k128;
 using gemm::store1;
 using gemm::tc_fence_after;
 using gemm::tc_fence_before;
 using gemm::tmem_ld32;
-using gemm::umma_commit;
 
-// Shared-memory descriptor of one scale tile for tcgen05.cp: 32 rows of 16
-// bytes, no swizzle, 8-row groups 128 bytes apart.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t addr)
+// One lane of a converged warp, the same one every time.  The issuing loops
+// below run in the whole warp and only the tcgen05 and copy instructions are
+// predicated on this lane: loop control, addresses and descriptors are then
+// uniform values.  With the loop inside `if (lane == 0)` every operand went
+// through a per-thread register first, and a step of 4 MMAs and 6 scale copies
+// took 0.87 us (4096 x 4096 x 4096) where its MMAs need 0.2.
+__device__ __forceinline__ uint32_t elect_one()
 {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+    uint32_t e;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
+    return e;
 }
+
+// Whole-warp bounded wait whose result is uniform.
+__device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+}
+
+// Shared-memory descriptors, the two 32-bit halves apart: codes (K-major,
+// 128-byte swizzle, 8-row groups 1024 bytes apart) and one scale tile (32 rows
+// of 16 bytes, no swizzle, 8-row groups 128 bytes apart).
+constexpr uint32_t kCodesDescHi = (1024u >> 4) | (1u << 14) | (2u << 29), kScaleDescHi = (128u >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint64_t desc64(uint32_t hi, uint32_t lo) { return ((uint64_t)hi << 32) | lo; }
 
 // 512 bytes (128 rows x 4 scales) to 4 columns of tensor memory, the 32 lanes
 // repeated for the four warps' quarters
-__device__ __forceinline__ void scale_copy(uint32_t taddr, uint64_t desc)
+template <bool PAIR>
+__device__ __forceinline__ void scale_copy(uint32_t lead, uint32_t taddr, uint64_t desc)
 {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    if constexpr (PAIR)
+        asm volatile("{ .reg .pred e; setp.ne.b32 e, %2, 0; @e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1; }" ::"r"(taddr), "l"(desc), "r"(lead)
+                     : "memory");
+    else
+        asm volatile("{ .reg .pred e; setp.ne.b32 e, %2, 0; @e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1; }" ::"r"(taddr), "l"(desc), "r"(lead)
+                     : "memory");
 }
 
 // Instruction descriptor of kind::mxf4nvf4: E2M1 operands (type code 1), K =
-// 64, scales E8M0 (1) or E4M3 (0); sf_id picks the first of the scale bytes
-// this instruction uses out of each 4-byte word (2 of 4 bytes per 64 elements
-// of MXFP4: 0 or 2; all 4 of NVFP4: 0).
-__host__ __device__ constexpr uint32_t idesc_fp4(bool nv, int M, int N, int sf_id)
+// 64, scales E8M0 (1) or E4M3 (0).  Scale ids 0 here: the ids (bits 4-5 and
+// 29-30) pick the first of the scale bytes that the instruction takes of each
+// 4-byte word (MXFP4 uses 2 per 64 elements, NVFP4 all 4).
+__host__ __device__ constexpr uint32_t idesc_fp4(bool nv, int M, int N)
 {
-    return ((uint32_t)sf_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((nv ? 0u : 1u) << 23) | ((uint32_t)(M >> 7) << 27) |
-           ((uint32_t)sf_id << 29);
+    return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((nv ? 0u : 1u) << 23) | ((uint32_t)(M >> 7) << 27);
 }
 
-template <bool NV>
-__device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t acc)
+#define RAZER_MX_MMA(GROUP, VEC)                                                                                                        \
+    asm volatile("{ .reg .pred p, e; setp.ne.b32 p, %4, 0; setp.ne.b32 e, %7, 0;\n"                                                      \
+                 "@e tcgen05.mma.cta_group::" GROUP ".kind::mxf4nvf4.block_scale.scale_vec::" VEC " [%0], %1, %2, %3, [%5], [%6], p; }" ::"r"(d),  \
+                 "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb), "r"(lead)                                                    \
+                 : "memory")
+template <bool NV, bool PAIR>
+__device__ __forceinline__ void umma_fp4(uint32_t lead, uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t acc)
 {
-    if constexpr (NV)
+    if constexpr (NV && PAIR) RAZER_MX_MMA("2", "4X");
+    else if constexpr (NV) RAZER_MX_MMA("1", "4X");
+    else if constexpr (PAIR) RAZER_MX_MMA("2", "2X");
+    else RAZER_MX_MMA("1", "2X");
+}
+#undef RAZER_MX_MMA
+
+// arrives on `bar` once the MMAs and copies issued so far are done (PAIR: on
+// the barrier at this offset in both CTAs)
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar)
+{
+    if constexpr (PAIR)
         asm volatile(
-            "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p; }" ::"r"(d),
-            "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)
+            "{ .reg .pred e; setp.ne.b32 e, %2, 0;\n"
+            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1; }" ::"r"(bar),
+            "h"((uint16_t)3), "r"(lead)
             : "memory");
     else
-        asm volatile(
-            "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p; }" ::"r"(d),
-            "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)
-            : "memory");
+        asm volatile("{ .reg .pred e; setp.ne.b32 e, %1, 0;\n"
+                     "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar),
+                     "r"(lead)
+                     : "memory");
+}
+
+constexpr int kStepK = 256;  // a stage is 128 bytes of codes per row
+template <bool NV> constexpr int kStepTiles = kStepK / (4 * (NV ? 16 : 32));  // scale tiles along a stage: 4 or 2
+
+// The copies and MMAs of one stage: `tiles` scale tiles and `ks` MMAs of 64 k
+// (the constants kStepTiles and 4 but in a last, partial stage).  SFB_TILES
+// tile rows of activation scales, `off2` the column of the first that the unit
+// uses.
+template <bool NV, bool PAIR, int SFB_TILES>
+__device__ __forceinline__ void issue_stage(uint32_t lead, uint32_t acc, uint32_t a0, uint32_t b0, uint32_t sa0, uint32_t sb0, uint32_t sfa,
+                                            uint32_t sfb, uint32_t off2, uint32_t idesc, bool fresh, int tiles, int ks)
+{
+    const uint32_t la = desc_lo(a0), lb = desc_lo(b0), lsa = desc_lo(sa0), lsb = desc_lo(sb0);
+#pragma unroll
+    for (int i = 0; i < kStepTiles<NV>; i++) {
+        if (i < tiles) {
+            scale_copy<PAIR>(lead, sfa + 4 * i, desc64(kScaleDescHi, lsa + i * (kTileBytes >> 4)));
+#pragma unroll
+            for (int j = 0; j < SFB_TILES; j++)
+                scale_copy<PAIR>(lead, sfb + 4 * SFB_TILES * i + 4 * j, desc64(kScaleDescHi, lsb + (j * kStepTiles<NV> + i) * (kTileBytes >> 4)));
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        if (k < ks) {
+            const int word = NV ? k : k >> 1;
+            // MXFP4: bytes 0-1 of a scale word, then 2-3 (scale ids 0 and 2)
+            const uint32_t id = idesc | ((!NV && (k & 1)) ? (2u << 4) | (2u << 29) : 0u);
+            umma_fp4<NV, PAIR>(lead, acc, desc64(kCodesDescHi, la + 2 * k), desc64(kCodesDescHi, lb + 2 * k), id, sfa + 4 * word,
+                               sfb + 4 * SFB_TILES * word + off2, (fresh && k == 0) ? 0u : 1u);
+        }
+    }
 }
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
@@ -83,21 +159,22 @@ struct Problem {
 };
 
 // Where a unit of work lies: rows row0 .. row0 + count - 1 of the activations
-// and the tile row where their scales start.
+// and the tile row, and the row in it, where their scales start.
 struct RowUnit {
-    int e, row0, count, trow;
+    int e, row0, count, trow, off;
 };
 
-// The t-th piece of up to `step` rows (a multiple of 128, so that its scales
-// start a tile row), counted over the groups; a warp works it out together,
-// 32 groups at a time.  count = 0: there is no such piece.
+// The t-th piece of up to `step` rows (a multiple of 64), counted over the
+// groups; a warp works it out together, 32 groups at a time.  count <= 0:
+// there is no such piece.
 __device__ __forceinline__ RowUnit row_unit(const Problem &p, int t, int step)
 {
-    RowUnit u = {0, 0, 0, 0};
+    RowUnit u = {0, 0, 0, 0, 0};
     if (p.E == 0) {
         u.row0 = t * step;
         u.count = min(step, p.T - u.row0);
         u.trow = u.row0 / kTileRows;
+        u.off = u.row0 % kTileRows;
         return u;
     }
     const int lane = threadIdx.x & 31;
@@ -128,11 +205,30 @@ __device__ __forceinline__ RowUnit row_unit(const Problem &p, int t, int step)
             u.row0 = start + in;
             u.count = min(step, n - in);
             u.trow = group_tile_row(start, u.e) + in / kTileRows;
+            u.off = in % kTileRows;
             return u;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);
     }
     return u;
+}
+
+// Writes 32 columns of an accumulator: lane `lane` holds output column n of
+// the rows row .. row + count - 1 (at most 32).  A warp's store covers 32
+// consecutive outputs of one row.
+template <typename TOut>
+__device__ __forceinline__ void write_columns(const float (&v)[32], float scale, const Problem &p, TOut *__restrict__ Y, int64_t ldy, int row,
+                                              int count, int n, int lane)
+{
+    TOut *y = Y + (int64_t)row * ldy + (p.gate ? n / 2 : n);
+    const bool mine = n < p.N && !(p.gate && (lane & 1));
+#pragma unroll
+    for (int i = 0; i < 32; i++) {
+        float a = v[i] * scale;
+        if (p.gate) a = silu_mul(a, __shfl_xor_sync(0xffffffffu, a, 1));  // row 2j gates row 2j + 1
+        if (mine && i < count) store1<TOut>(y, a);
+        y += ldy;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -146,8 +242,6 @@ __device__ __forceinline__ RowUnit row_unit(const Problem &p, int t, int step)
 // Stage: 256 k of 128 weight rows (16 KB) and of the activation rows, and the
 // scale tiles of both.
 // ---------------------------------------------------------------------------
-constexpr int kStepK = 256;  // a stage is 128 bytes of codes per row
-template <bool NV> constexpr int kStepTiles = kStepK / (4 * (NV ? 16 : 32));  // scale tiles along a stage: 4 or 2
 constexpr int kStreamThreads = 192;
 
 constexpr int kStreamRows = 128, kBoxRows = 32;
@@ -259,43 +353,36 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && nk > 0) {
+        if (nk > 0) {
             // ---------------- MMA issuer ----------------
-            const int n = (count + 7) & ~7;  // the MMA's width: a multiple of 8
-            const uint32_t id0 = idesc_fp4(NV, 128, n, 0), id2 = idesc_fp4(NV, 128, n, 2);
+            const uint32_t lead = elect_one();
+            const uint32_t idesc = idesc_fp4(NV, 128, (count + 7) & ~7);  // the MMA's width: a multiple of 8
+            const int tail_tiles = p.ct - (nk - 1) * kStepTiles<NV>, tail_ks = (p.K - (nk - 1) * kStepK + 63) / 64;
             uint32_t s = 0, ph = 0;
             bool ok = true;
             for (int g = 0; g < nk; g++) {
-                if (!mbar_wait(full + 8 * s, ph, abort_flag)) {
+                if (!mbar_wait_all(full + 8 * s, ph, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t a0 = smem_addr(smem) + s * stage, b0 = a0 + Cfg::kA;
+                const uint32_t a0 = smem_addr(smem) + s * stage, b0 = a0 + Cfg::kA, s0 = b0 + bbytes;
                 const uint32_t sfa = tmem + kStreamRows + (uint32_t)(g & 1) * 2 * Cfg::kScaleCols, sfb = sfa + Cfg::kScaleCols;
-                const int nt = min(kStepTiles<NV>, p.ct - g * kStepTiles<NV>);
-                for (int i = 0; i < nt; i++) {
-                    scale_copy(sfa + 4 * i, scale_desc(b0 + bbytes + i * kTileBytes));
-                    scale_copy(sfb + 4 * i, scale_desc(b0 + bbytes + Cfg::kS + i * kTileBytes));
-                }
-                const int ks = min(4, (p.K - g * kStepK + 63) / 64);  // MMAs of 64 k that hold any of K
-                for (int k = 0; k < ks; k++) {
-                    const int word = NV ? k : k >> 1;
-                    umma_fp4<NV>(tmem, smem_desc_k128(a0 + 32 * k), smem_desc_k128(b0 + 32 * k), (!NV && (k & 1)) ? id2 : id0, sfa + 4 * word,
-                                 sfb + 4 * word, (g > 0 || k > 0) ? 1u : 0u);
-                }
-                umma_commit(empty + 8 * s);
+                if (g + 1 < nk) issue_stage<NV, false, 1>(lead, tmem, a0, b0, s0, s0 + Cfg::kS, sfa, sfb, 0u, idesc, g == 0, kStepTiles<NV>, 4);
+                else issue_stage<NV, false, 1>(lead, tmem, a0, b0, s0, s0 + Cfg::kS, sfa, sfb, 0u, idesc, g == 0, tail_tiles, tail_ks);
+                commit<false>(lead, empty + 8 * s);
                 if (++s == stages) {
                     s = 0;
                     ph ^= 1u;
                 }
             }
-            if (ok) umma_commit(acc_full);
+            if (ok) commit<false>(lead, acc_full);
             // every MMA issued has completed before the tensor memory is freed (bounded)
-            umma_commit(drained);
+            commit<false>(lead, drained);
             const uint64_t t0 = globaltimer();
             while (!mbar_try_wait(drained, 0) && globaltimer() - t0 < kTimeoutNs) {
             }
+            __syncwarp();
         }
     } else if (count > 0) {
         // ---------------- epilogue ----------------
@@ -311,17 +398,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             for (int c0 = 0; c0 < count; c0 += 32) {
                 float v[32];
                 tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0, v);
-#pragma unroll
-                for (int i = 0; i < 32; i++) {
-                    float y = v[i] * scale;
-                    if (p.gate) {
-                        // row 2j gates row 2j + 1
-                        const float up = __shfl_xor_sync(0xffffffffu, y, 1);
-                        if (c0 + i < count && n < p.N && !(lane & 1)) store1<TOut>(Y + (int64_t)(row0 + c0 + i) * ldy + n / 2, silu_mul(y, up));
-                    } else if (c0 + i < count && n < p.N) {
-                        store1<TOut>(Y + (int64_t)(row0 + c0 + i) * ldy + n, y);
-                    }
-                }
+write_columns<TOut>(v, scale, p, Y, ldy, row0 + c0, count - c0, n, lane);
             }
         }
         tc_fence_before();
@@ -331,6 +408,249 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(Cfg::kCols));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// mx_pair_kernel: many rows per group.  A persistent cluster of two CTAs per
+// 256 weight rows x up to 192 activation rows (cta_group::2: one MMA of M =
+// 256 over both SMs, each CTA holding its 128 weight rows, half of the
+// activation rows and 128 lanes of the accumulator).  Sharing the activation
+// rows is what the FP4 rate asks for: an SM's operands per 256 k are (128 +
+// 96) x 128 bytes for 384 cycles of MMA, 75 bytes a cycle, where one CTA
+// alone would need 107.
+//   warp 0: bulk-tensor producer (each CTA loads its own operands; the
+//   leader's barrier counts both); warp 1: tensor memory, and in the leader
+//   the MMA issuer; warps 2-5: epilogue, a quarter of the lanes each.
+// Two accumulators of 192 columns: the epilogue of a unit runs beside the MMAs
+// of the next.  384 + 2 x 24 (NVFP4: 2 x 48) columns of scales fit in 512;
+// 256-wide accumulators would leave no room for them.
+// A unit's rows start at a multiple of 64 rows of their group, so its scales
+// start at column 0 or 2 of their tile.
+// ---------------------------------------------------------------------------
+constexpr int kPairRows = 192, kPairThreads = 192;
+
+template <bool NV> struct PairCfg {
+    static constexpr uint32_t kA = 128 * 128, kB = kPairRows / 2 * 128, kS = kStepTiles<NV> * kTileBytes;
+    static constexpr uint32_t kStage = kA + kB + 3 * kS;  // scales: own weight rows, and two tile rows of activations
+    static constexpr int kStages = (int)((232448u - 1024u - 512u) / kStage);
+    static constexpr uint32_t kSmem = kStages * kStage + 512u + 1024u;
+    static constexpr uint32_t kSfaCols = kStepTiles<NV> * 4, kSfbCols = kStepTiles<NV> * 8;
+    static_assert(2 * kPairRows + 2 * (kSfaCols + kSfbCols) <= 512, "tensor memory");
+    static_assert(16 * kStages + 40 <= 256, "barriers");
+};
+
+// shared-memory address of the same object in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// loads into this CTA's shared memory that count on a barrier of either CTA of the pair
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t lead, uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar)
+{
+    asm volatile(
+        "{ .reg .pred e; setp.ne.b32 e, %5, 0;\n"
+        "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4]; }" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t lead, uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar)
+{
+    asm volatile(
+        "{ .reg .pred e; setp.ne.b32 e, %6, 0;\n"
+        "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5]; }" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx_one(uint32_t lead, uint32_t bar, uint32_t bytes)
+{
+    asm volatile("{ .reg .pred e; setp.ne.b32 e, %2, 0; @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1; }" ::"r"(bar), "r"(bytes), "r"(lead)
+                 : "memory");
+}
+template <bool NV, typename TOut>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    mx_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a,
+                   const __grid_constant__ CUtensorMap tmap_sw, const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ Problem p,
+                   int ntiles, int step, TOut *__restrict__ Y, int inject_stall)
+{
+    using Cfg = PairCfg<NV>;
+    constexpr int STAGES = Cfg::kStages;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *bars = smem + STAGES * Cfg::kStage;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * STAGES, acc_full = empty + 8 * STAGES, acc_empty = acc_full + 16,
+                   drained = acc_empty + 16;
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + 256);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 260);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; s++) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; b++) {
+            mbar_init(acc_full + 8 * b, 1);
+            mbar_init(acc_empty + 8 * b, 8);  // the epilogue warps of both CTAs
+        }
+        mbar_init(drained, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr((const void *)tmem_slot)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers and tensor memory are ready
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();  // the activations come from an earlier kernel of the stream
+    if (p.E > 0 && blockIdx.x == 0) check_offsets(p.offsets, p.E, p.T);
+    const int nk = (p.K + kStepK - 1) / kStepK;
+
+    if (warp == 0) {
+        // ---------------- producer ----------------
+        const uint32_t lead = elect_one(), full0 = cluster_addr(full, 0);
+        uint32_t s = 0, ph = 0;
+        bool ok = true, first = true;
+        for (int u = pair; ok; u += pairs) {
+            const RowUnit w = row_unit(p, u / ntiles, step);
+            if (w.count <= 0) break;
+            const int n0 = (u % ntiles) * 256 + (int)rank * 128;
+            const int arow = w.row0 + (int)rank * (((w.count + 15) & ~15) / 2);  // each CTA holds half of the unit's rows
+            const int wrow = w.e * p.N + n0;
+            // a weight tile row that does not exist: any other will do, its rows are not written
+            const int srow = w.e * p.trows_w + min(n0 / kTileRows, p.trows_w - 1);
+            for (int g = 0; g < nk; g++) {
+                if (!mbar_wait_all(empty + 8 * s, ph ^ 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                // fault injection (tests only): the first CTA never fills its first stage
+                const bool stall = inject_stall && blockIdx.x == 0 && first;
+                first = false;
+                if (!stall) {
+                    const uint32_t a0 = smem_addr(smem) + s * Cfg::kStage, f = full0 + 8 * s, s0 = a0 + Cfg::kA + Cfg::kB;
+                    if (rank == 0) mbar_expect_tx_one(lead, full + 8 * s, 2 * Cfg::kStage);
+                    tma_load_2d_pair(lead, a0, &tmap_w, g * 128, wrow, f);
+                    tma_load_2d_pair(lead, a0 + Cfg::kA, &tmap_a, g * 128, arow, f);
+                    tma_load_3d_pair(lead, s0, &tmap_sw, 0, g * kStepTiles<NV> * 2, srow, f);
+                    tma_load_3d_pair(lead, s0 + Cfg::kS, &tmap_sa, 0, g * kStepTiles<NV> * 2, w.trow, f);
+                }
+                if (++s == STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        if (!ok) {
+            // loads already issued land within microseconds; they count on the
+            // leader's barrier, which may never complete: wait a fixed 2 ms
+            const uint64_t t0 = globaltimer();
+            while (globaltimer() - t0 < 2000000ull) {
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            // ---------------- MMA issuer (leader) ----------------
+            const uint32_t lead = elect_one();
+            const int tail_tiles = p.ct - (nk - 1) * kStepTiles<NV>, tail_ks = (p.K - (nk - 1) * kStepK + 63) / 64;
+            uint32_t s = 0, ph = 0, ti = 0;
+            bool ok = true;
+            for (int u = pair; ok; u += pairs, ti++) {
+                const RowUnit w = row_unit(p, u / ntiles, step);
+                if (w.count <= 0) break;
+                const uint32_t b = ti & 1u, acc = tmem + b * kPairRows;
+                // the epilogue has drained this accumulator
+                if (!mbar_wait_all(acc_empty + 8 * b, ((ti >> 1) & 1u) ^ 1u, abort_flag)) break;
+                tc_fence_after();
+                const uint32_t idesc = idesc_fp4(NV, 256, (w.count + 15) & ~15), off2 = (uint32_t)w.off >> 5;
+                for (int g = 0; g < nk; g++) {
+                    if (!mbar_wait_all(full + 8 * s, ph, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a0 = smem_addr(smem) + s * Cfg::kStage, b0 = a0 + Cfg::kA, s0 = b0 + Cfg::kB;
+                    const uint32_t sfa = tmem + 2 * kPairRows + (uint32_t)(g & 1) * (Cfg::kSfaCols + Cfg::kSfbCols), sfb = sfa + Cfg::kSfaCols;
+                    if (g + 1 < nk)
+                        issue_stage<NV, true, 2>(lead, acc, a0, b0, s0, s0 + Cfg::kS, sfa, sfb, off2, idesc, g == 0, kStepTiles<NV>, 4);
+                    else
+                        issue_stage<NV, true, 2>(lead, acc, a0, b0, s0, s0 + Cfg::kS, sfa, sfb, off2, idesc, g == 0, tail_tiles, tail_ks);
+                    commit<true>(lead, empty + 8 * s);
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (ok) commit<true>(lead, acc_full + 8 * b);
+            }
+            // every MMA issued has completed before the tensor memory is freed (bounded)
+            asm volatile("{ .reg .pred e; setp.ne.b32 e, %1, 0; @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(
+                             drained),
+                         "r"(lead)
+                         : "memory");
+            const uint64_t t0 = globaltimer();
+            while (!mbar_try_wait(drained, 0) && globaltimer() - t0 < kTimeoutNs) {
+            }
+            __syncwarp();
+        }
+    } else {
+        // ---------------- epilogue ----------------
+        const int q = warp & 3;
+        const uint32_t acc_empty0 = cluster_addr(acc_empty, 0);
+        const int64_t ldy = p.gate ? p.N / 2 : p.N;
+        const float ts_a = p.ts_a ? *p.ts_a : 1.0f;
+        uint32_t ti = 0;
+        for (int u = pair;; u += pairs, ti++) {
+            const RowUnit w = row_unit(p, u / ntiles, step);
+            if (w.count <= 0) break;
+            const uint32_t b = ti & 1u;
+            if (!mbar_wait_warp(acc_full + 8 * b, (ti >> 1) & 1u, abort_flag)) break;
+            tc_fence_after();
+            const int n = (u % ntiles) * 256 + (int)rank * 128 + q * 32 + lane;
+            const float scale = p.ts_w ? __fmul_rn(ts_a, p.ts_w[w.e]) : ts_a;
+#pragma unroll 1
+            for (int c0 = 0; c0 < w.count; c0 += 32) {
+                float v[32];
+                tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + b * kPairRows + (uint32_t)c0, v);
+                if (c0 + 32 >= w.count) {
+                    // this warp has read the whole accumulator: hand it back
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8 * b);
+                }
+                write_columns<TOut>(v, scale, p, Y, ldy, w.row0 + c0, w.count - c0, n, lane);
+            }
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    __syncthreads();
+    cluster_sync();  // no CTA leaves while the other may still signal its barriers
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
 }
 
@@ -354,6 +674,19 @@ static bool encode_codes_map(CUtensorMap *map, const void *base, int64_t rows, i
     const cuuint32_t es[2] = {1u, 1u};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// scale tiles [tile rows][ct tiles] as rows of 256 bytes, read in boxes of `rows` x `tiles` tiles
+static bool encode_tiles_map(CUtensorMap *map, const void *base, int64_t trows, int64_t ct, int rows, int tiles)
+{
+    const EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {256u, (cuuint64_t)(2 * ct), (cuuint64_t)trows};
+    const cuuint64_t strides[2] = {256u, (cuuint64_t)(ct * kTileBytes)};
+    const cuuint32_t box[3] = {256u, (cuuint32_t)(2 * tiles), (cuuint32_t)rows};
+    const cuuint32_t es[3] = {1u, 1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // pieces of `step` rows that T rows in E groups can make
@@ -384,8 +717,51 @@ static razer_status launch_stream(const uint8_t *codes_a, const uint8_t *codes_w
 }
 
 template <bool NV, typename TOut>
+static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, int step, TOut *Y, cudaStream_t st)
+{
+    using Cfg = PairCfg<NV>;
+    static int resident[64] = {0};  // clusters that the device holds at once
+    int dev = 0;
+    cudaGetDevice(&dev);
+    int pairs = dev >= 0 && dev < 64 ? resident[dev] : 0;
+    if (pairs == 0) {
+        if (cudaFuncSetAttribute(mx_pair_kernel<NV, TOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmem) != cudaSuccess)
+            return RAZER_ERR_CUDA;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(sm_count() & ~1));
+        cfg.blockDim = dim3(kPairThreads);
+        cfg.dynamicSmemBytes = Cfg::kSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&pairs, mx_pair_kernel<NV, TOut>, &cfg) != cudaSuccess || pairs < 1) return RAZER_ERR_CUDA;
+        pairs = std::min(pairs, sm_count() / 2);
+        if (dev >= 0 && dev < 64) resident[dev] = pairs;
+    }
+    CUtensorMap mw, ma, msw, msa;
+    const int64_t E = p.E ? p.E : 1, arows = p.E ? tile_rows_grouped(p.T, p.E) : tile_rows(p.T);
+    if (!encode_codes_map(&mw, codes_w, p.N * E, p.K, 128) || !encode_codes_map(&ma, codes_a, p.T, p.K, kPairRows / 2) ||
+        !encode_tiles_map(&msw, p.tiles_w, E * p.trows_w, p.ct, 1, kStepTiles<NV>) ||
+        !encode_tiles_map(&msa, p.tiles_a, arows, p.ct, 2, kStepTiles<NV>))
+        return RAZER_ERR_CUDA;
+    const int ntiles = (p.N + 255) / 256;
+    const int64_t units = max_pieces(p.T, p.E, step) * ntiles;
+    if (units > INT32_MAX - 1024) return RAZER_ERR_SHAPE;
+    const int inject = fault_injection_enabled() ? 1 : 0;
+    if (launch_pdl(mx_pair_kernel<NV, TOut>, 2u * (unsigned)std::min<int64_t>(units, pairs), (unsigned)kPairThreads, (size_t)Cfg::kSmem, st, mw,
+                   ma, msw, msa, p, ntiles, step, Y, inject) != cudaSuccess)
+        return RAZER_ERR_CUDA;
+    return RAZER_OK;
+}
+
+template <bool NV, typename TOut>
 static razer_status launch_mx(const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, TOut *Y, cudaStream_t st)
 {
+    const int64_t rows = p.E > 0 ? (p.T + p.E - 1) / p.E : p.T;  // rows of a group, on average
+    if (rows > 64) return launch_pair<NV, TOut>(codes_a, codes_w, p, kPairRows, Y, st);
     return launch_stream<NV, TOut>(codes_a, codes_w, p, Y, st);
 }
 

@@ -140,7 +140,8 @@ def factor(ts_a, ts_w, e=0):
 
 
 SIZES = [(1, 128, 256), (8, 128, 64), (7, 40, 32), (16, 200, 96), (1, 1, 160), (33, 257, 512), (32, 128, 288), (65, 64, 1024), (64, 130, 480),
-         (128, 128, 4128), (129, 300, 352), (300, 72, 640), (2, 512, 8192), (500, 600, 768)]
+         (128, 128, 4128), (129, 300, 352), (300, 72, 640), (2, 512, 8192), (500, 600, 768),
+         (200, 256, 2048), (1500, 2600, 320), (700, 6000, 1088)]
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
@@ -216,7 +217,7 @@ def test_product_nan_scale_reaches_its_row_only():
 
 
 GROUPS = [([3, 0, 1, 5], 0, 0), ([0, 0, 0], 2, 3), ([1] * 40, 1, 2), ([33, 0, 2, 64, 31], 5, 9), ([130, 260, 0, 7], 0, 4), ([0, 513], 0, 0),
-          ([70, 70, 70, 0, 1, 200], 11, 30)]
+          ([70, 70, 70, 0, 1, 200], 11, 30), ([700, 3, 0, 1000, 190, 193, 65], 1, 2)]
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
