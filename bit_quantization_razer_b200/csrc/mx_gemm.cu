@@ -33,10 +33,10 @@ using gemm::tmem_ld32;
 
 // One lane of a converged warp, the same one every time.  The issuing loops
 // below run in the whole warp and only the tcgen05 and copy instructions are
-// predicated on this lane: loop control, addresses and descriptors are then
-// uniform values.  With the loop inside `if (lane == 0)` every operand went
-// through a per-thread register first, and a step of 4 MMAs and 6 scale copies
-// took 0.87 us (4096 x 4096 x 4096) where its MMAs need 0.2.
+// left to this lane: loop control, addresses and descriptors are then uniform
+// values.  With the whole loop inside `if (lane == 0)` every operand went
+// through a per-thread register first, and a stage of 4 MMAs and 6 scale
+// copies took 0.87 us (4096 x 4096 x 4096) where its MMAs need 0.2.
 __device__ __forceinline__ uint32_t elect_one()
 {
     uint32_t e;
@@ -59,16 +59,12 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return ((addr & 0x3
 __device__ __forceinline__ uint64_t desc64(uint32_t hi, uint32_t lo) { return ((uint64_t)hi << 32) | lo; }
 
 // 512 bytes (128 rows x 4 scales) to 4 columns of tensor memory, the 32 lanes
-// repeated for the four warps' quarters
+// repeated for the four warps' quarters (one lane issues)
 template <bool PAIR>
-__device__ __forceinline__ void scale_copy(uint32_t lead, uint32_t taddr, uint64_t desc)
+__device__ __forceinline__ void scale_copy(uint32_t taddr, uint64_t desc)
 {
-    if constexpr (PAIR)
-        asm volatile("{ .reg .pred e; setp.ne.b32 e, %2, 0; @e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1; }" ::"r"(taddr), "l"(desc), "r"(lead)
-                     : "memory");
-    else
-        asm volatile("{ .reg .pred e; setp.ne.b32 e, %2, 0; @e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1; }" ::"r"(taddr), "l"(desc), "r"(lead)
-                     : "memory");
+    if constexpr (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 // Instruction descriptor of kind::mxf4nvf4: E2M1 operands (type code 1), K =
@@ -81,13 +77,12 @@ __host__ __device__ constexpr uint32_t idesc_fp4(bool nv, int M, int N)
 }
 
 #define RAZER_MX_MMA(GROUP, VEC)                                                                                                        \
-    asm volatile("{ .reg .pred p, e; setp.ne.b32 p, %4, 0; setp.ne.b32 e, %7, 0;\n"                                                      \
-                 "@e tcgen05.mma.cta_group::" GROUP ".kind::mxf4nvf4.block_scale.scale_vec::" VEC " [%0], %1, %2, %3, [%5], [%6], p; }" ::"r"(d),  \
-                 "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb), "r"(lead)                                                    \
+    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"                                                                               \
+                 "tcgen05.mma.cta_group::" GROUP ".kind::mxf4nvf4.block_scale.scale_vec::" VEC " [%0], %1, %2, %3, [%5], [%6], p; }" ::"r"(d),  \
+                 "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)                                                               \
                  : "memory")
 template <bool NV, bool PAIR>
-__device__ __forceinline__ void umma_fp4(uint32_t lead, uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                         uint32_t acc)
+__device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t acc)
 {
     if constexpr (NV && PAIR) RAZER_MX_MMA("2", "4X");
     else if constexpr (NV) RAZER_MX_MMA("1", "4X");
@@ -117,31 +112,39 @@ __device__ __forceinline__ void commit(uint32_t lead, uint32_t bar)
 constexpr int kStepK = 256;  // a stage is 128 bytes of codes per row
 template <bool NV> constexpr int kStepTiles = kStepK / (4 * (NV ? 16 : 32));  // scale tiles along a stage: 4 or 2
 
-// The copies and MMAs of one stage: `tiles` scale tiles and `ks` MMAs of 64 k
-// (the constants kStepTiles and 4 but in a last, partial stage).  SFB_TILES
-// tile rows of activation scales, `off2` the column of the first that the unit
-// uses.
+// The scale copies of one stage: kStepTiles tiles of the weights and of
+// SFB_TILES tile rows of the activations.  A stage is always whole: the loads
+// fill what lies past K with zero codes and zero scale bytes (0 or 2^-127,
+// finite), which add nothing.
 template <bool NV, bool PAIR, int SFB_TILES>
-__device__ __forceinline__ void issue_stage(uint32_t lead, uint32_t acc, uint32_t a0, uint32_t b0, uint32_t sa0, uint32_t sb0, uint32_t sfa,
-                                            uint32_t sfb, uint32_t off2, uint32_t idesc, bool fresh, int tiles, int ks)
+__device__ __forceinline__ void issue_scales(uint32_t lead, uint32_t sa0, uint32_t sb0, uint32_t sfa, uint32_t sfb)
 {
-    const uint32_t la = desc_lo(a0), lb = desc_lo(b0), lsa = desc_lo(sa0), lsb = desc_lo(sb0);
+    const uint32_t lsa = desc_lo(sa0), lsb = desc_lo(sb0);
+    if (lead) {
 #pragma unroll
-    for (int i = 0; i < kStepTiles<NV>; i++) {
-        if (i < tiles) {
-            scale_copy<PAIR>(lead, sfa + 4 * i, desc64(kScaleDescHi, lsa + i * (kTileBytes >> 4)));
+        for (int i = 0; i < kStepTiles<NV>; i++) {
+            scale_copy<PAIR>(sfa + 4 * i, desc64(kScaleDescHi, lsa + i * (kTileBytes >> 4)));
 #pragma unroll
             for (int j = 0; j < SFB_TILES; j++)
-                scale_copy<PAIR>(lead, sfb + 4 * SFB_TILES * i + 4 * j, desc64(kScaleDescHi, lsb + (j * kStepTiles<NV> + i) * (kTileBytes >> 4)));
+                scale_copy<PAIR>(sfb + 4 * SFB_TILES * i + 4 * j, desc64(kScaleDescHi, lsb + (j * kStepTiles<NV> + i) * (kTileBytes >> 4)));
         }
     }
+}
+
+// The four MMAs of a stage, 64 k each; off2: the column of the activations'
+// first scale tile that the unit starts at.
+template <bool NV, bool PAIR, int SFB_TILES>
+__device__ __forceinline__ void issue_mmas(uint32_t lead, uint32_t acc, uint32_t a0, uint32_t b0, uint32_t sfa, uint32_t sfb, uint32_t off2,
+                                           uint32_t idesc, bool fresh)
+{
+    const uint32_t la = desc_lo(a0), lb = desc_lo(b0);
+    if (lead) {
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-        if (k < ks) {
+        for (int k = 0; k < 4; k++) {
             const int word = NV ? k : k >> 1;
             // MXFP4: bytes 0-1 of a scale word, then 2-3 (scale ids 0 and 2)
             const uint32_t id = idesc | ((!NV && (k & 1)) ? (2u << 4) | (2u << 29) : 0u);
-            umma_fp4<NV, PAIR>(lead, acc, desc64(kCodesDescHi, la + 2 * k), desc64(kCodesDescHi, lb + 2 * k), id, sfa + 4 * word,
+            umma_fp4<NV, PAIR>(acc, desc64(kCodesDescHi, la + 2 * k), desc64(kCodesDescHi, lb + 2 * k), id, sfa + 4 * word,
                                sfb + 4 * SFB_TILES * word + off2, (fresh && k == 0) ? 0u : 1u);
         }
     }
@@ -157,6 +160,14 @@ struct Problem {
     const int32_t *offsets;
     int E, T, N, K, ct, trows_w, gate;
 };
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
 
 // Where a unit of work lies: rows row0 .. row0 + count - 1 of the activations
 // and the tile row, and the row in it, where their scales start.
@@ -213,21 +224,51 @@ __device__ __forceinline__ RowUnit row_unit(const Problem &p, int t, int step)
     return u;
 }
 
-// Writes 32 columns of an accumulator: lane `lane` holds output column n of
-// the rows row .. row + count - 1 (at most 32).  A warp's store covers 32
-// consecutive outputs of one row.
-template <typename TOut>
-__device__ __forceinline__ void write_columns(const float (&v)[32], float scale, const Problem &p, TOut *__restrict__ Y, int64_t ldy, int row,
-                                              int count, int n, int lane)
+// two adjacent 16-bit outputs (4-byte aligned)
+template <typename TOut> __device__ __forceinline__ void store_pair(TOut *p, float a, float b)
 {
-    TOut *y = Y + (int64_t)row * ldy + (p.gate ? n / 2 : n);
-    const bool mine = n < p.N && !(p.gate && (lane & 1));
+    if constexpr (sizeof(TOut) == 2) *reinterpret_cast<unsigned *>(p) = Out16<TOut>::pack(a, b);
+}
+
+// Writes 32 columns of an accumulator: lane `lane` holds output column n of
+// the rows row .. row + count - 1 (at most 32).  Adjacent lanes swap halves of
+// two columns, so that the even lane finishes the first row and the odd lane
+// the second: a gated pair meets in one lane and every lane computes one, and
+// 16-bit outputs leave in pairs, 16 stores instead of 32.  (One store per
+// column and lane, the gate tested inside the loop: 15,700 cycles for a unit
+// of 192 rows, twice what its 16 stages of MMAs take.)
+template <typename TOut, bool GATE>
+__device__ __forceinline__ void write_columns(const float (&v)[32], float scale, int N, TOut *__restrict__ Y, int64_t ldy, int row, int count,
+                                              int n, int lane)
+{
+    const int odd = lane & 1;
+    if constexpr (GATE) {
+        // row 2j of the weights gates row 2j + 1
+        TOut *y = Y + (int64_t)(row + odd) * ldy + n / 2;
 #pragma unroll
-    for (int i = 0; i < 32; i++) {
-        float a = v[i] * scale;
-        if (p.gate) a = silu_mul(a, __shfl_xor_sync(0xffffffffu, a, 1));  // row 2j gates row 2j + 1
-        if (mine && i < count) store1<TOut>(y, a);
-        y += ldy;
+        for (int i = 0; i < 32; i += 2) {
+            const float mine = (odd ? v[i + 1] : v[i]) * scale, give = (odd ? v[i] : v[i + 1]) * scale;
+            const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+            const float a = odd ? silu_mul(got, mine) : silu_mul(mine, got);
+            if (n < N && i + odd < count) store1<TOut>(y, a);
+            y += 2 * ldy;
+        }
+    } else if (sizeof(TOut) == 2 && (ldy & 1) == 0) {
+        TOut *y = Y + (int64_t)(row + odd) * ldy + (n & ~1);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const float mine = (odd ? v[i + 1] : v[i]) * scale, give = (odd ? v[i] : v[i + 1]) * scale;
+            const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+            if (n < N && i + odd < count) store_pair<TOut>(y, odd ? got : mine, odd ? mine : got);
+            y += 2 * ldy;
+        }
+    } else {
+        TOut *y = Y + (int64_t)row * ldy + n;
+#pragma unroll
+        for (int i = 0; i < 32; i++) {
+            if (n < N && i < count) store1<TOut>(y, v[i] * scale);
+            y += ldy;
+        }
     }
 }
 
@@ -251,17 +292,18 @@ constexpr int kStreamMaxStages = 8;
 
 template <bool NV> struct StreamCfg {
     static constexpr uint32_t kA = 128 * 128, kBox = kBoxRows * 128, kS = kStepTiles<NV> * kTileBytes;
-    // tensor memory: accumulator, then two sets of scales (A, B)
+    // tensor memory: accumulator, then the scales of a stage (weights, activations)
     static constexpr uint32_t kScaleCols = kStepTiles<NV> * 4;
     static constexpr uint32_t kCols = 256;
-    static_assert(kStreamRows + 4 * kScaleCols <= kCols, "two CTAs share an SM's tensor memory");
+    static_assert(kStreamRows + 2 * kScaleCols <= kCols, "two CTAs share an SM's tensor memory");
     static_assert(kStreamRing / (kA + kBox + 2 * kS) <= kStreamMaxStages, "barriers for every stage");
     static_assert(kStreamRing / (kA + kStreamRows * 128 + 2 * kS) >= 3, "a ring for the widest unit");
 };
 
-template <bool NV, typename TOut>
+template <bool NV, typename TOut, bool GATE>
 __global__ void __launch_bounds__(kStreamThreads, 2)
-    mx_stream_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ Problem p,
+    mx_stream_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a,
+                     const __grid_constant__ CUtensorMap tmap_sw, const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ Problem p,
                      int ntiles, TOut *__restrict__ Y, int inject_stall)
 {
     using Cfg = StreamCfg<NV>;
@@ -312,52 +354,48 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     const uint32_t stages = kStreamRing / stage;
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---------------- producer ----------------
-            const uint8_t *sw = p.tiles_w + ((int64_t)ue * p.trows_w + n0 / kTileRows) * p.ct * kTileBytes;
-            const uint8_t *sa = p.tiles_a + (int64_t)trow * p.ct * kTileBytes;
-            const int wrow = ue * p.N + n0;
-            int g = 0;
-            uint32_t s = 0, ph = 0;  // the ring: stage, how often it went round
-            bool ok = true;
-            for (; g < nk; g++) {
-                if (!mbar_wait(empty + 8 * s, ph ^ 1u, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                // fault injection (tests only): the first CTA never fills its first stage
-                const bool stall = inject_stall && blockIdx.x == 0 && g == 0;
-                const uint32_t a0 = smem_addr(smem) + s * stage, f = full + 8 * s;
-                const int c0 = g * kStepTiles<NV>;
-                const uint32_t sbytes = (uint32_t)min(kStepTiles<NV>, p.ct - c0) * kTileBytes;
-                if (!stall) {
-                    mbar_expect_tx(f, Cfg::kA + bbytes + 2 * sbytes);
-                    tma_load_2d(a0, &tmap_w, g * 128, wrow, f);
-                    for (int b = 0; b < boxes; b++) tma_load_2d(a0 + Cfg::kA + b * Cfg::kBox, &tmap_a, g * 128, row0 + b * kBoxRows, f);
-                    bulk_load(a0 + Cfg::kA + bbytes, sw + (int64_t)c0 * kTileBytes, sbytes, f);
-                    bulk_load(a0 + Cfg::kA + bbytes + Cfg::kS, sa + (int64_t)c0 * kTileBytes, sbytes, f);
-                }
-                if (++s == stages) {
-                    s = 0;
-                    ph ^= 1u;
+        // ---------------- producer ----------------
+        const uint32_t lead = elect_one();
+        const int wrow = ue * p.N + n0, srow = ue * p.trows_w + n0 / kTileRows;
+        int g = 0;
+        uint32_t s = 0, ph = 0;  // the ring: stage, how often it went round
+        bool ok = true;
+        for (; g < nk; g++) {
+            if (!mbar_wait_all(empty + 8 * s, ph ^ 1u, abort_flag)) {
+                ok = false;
+                break;
+            }
+            // fault injection (tests only): the first CTA never fills its first stage
+            const bool stall = inject_stall && blockIdx.x == 0 && g == 0;
+            const uint32_t a0 = smem_addr(smem) + s * stage, f = full + 8 * s, s0 = a0 + Cfg::kA + bbytes;
+            if (lead && !stall) {
+                mbar_expect_tx(f, stage);
+                tma_load_2d(a0, &tmap_w, g * 128, wrow, f);
+                tma_load_3d(s0, &tmap_sw, 0, g * kStepTiles<NV> * 2, srow, f);
+                for (int b = 0; b < boxes; b++) tma_load_2d(a0 + Cfg::kA + b * Cfg::kBox, &tmap_a, g * 128, row0 + b * kBoxRows, f);
+                tma_load_3d(s0 + Cfg::kS, &tmap_sa, 0, g * kStepTiles<NV> * 2, trow, f);
+            }
+            if (++s == stages) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+        if (!ok) {
+            // let the loads already issued land before the CTA exits (bounded)
+            const uint64_t t0 = globaltimer();
+            for (int gg = g > (int)stages ? g - (int)stages : 0; gg < g; gg++) {
+                if (inject_stall && blockIdx.x == 0 && gg == 0) continue;
+                while (!mbar_try_wait(full + 8 * ((uint32_t)gg % stages), ((uint32_t)gg / stages) & 1u) && globaltimer() - t0 < kTimeoutNs) {
                 }
             }
-            if (!ok) {
-                // let the loads already issued land before the CTA exits (bounded)
-                const uint64_t t0 = globaltimer();
-                for (int gg = g > (int)stages ? g - (int)stages : 0; gg < g; gg++) {
-                    if (inject_stall && blockIdx.x == 0 && gg == 0) continue;
-                    while (!mbar_try_wait(full + 8 * ((uint32_t)gg % stages), ((uint32_t)gg / stages) & 1u) && globaltimer() - t0 < kTimeoutNs) {
-                    }
-                }
-            }
+            __syncwarp();
         }
     } else if (warp == 1) {
         if (nk > 0) {
             // ---------------- MMA issuer ----------------
             const uint32_t lead = elect_one();
             const uint32_t idesc = idesc_fp4(NV, 128, (count + 7) & ~7);  // the MMA's width: a multiple of 8
-            const int tail_tiles = p.ct - (nk - 1) * kStepTiles<NV>, tail_ks = (p.K - (nk - 1) * kStepK + 63) / 64;
+            const uint32_t sfa = tmem + kStreamRows, sfb = sfa + Cfg::kScaleCols;
             uint32_t s = 0, ph = 0;
             bool ok = true;
             for (int g = 0; g < nk; g++) {
@@ -367,9 +405,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
                 }
                 tc_fence_after();
                 const uint32_t a0 = smem_addr(smem) + s * stage, b0 = a0 + Cfg::kA, s0 = b0 + bbytes;
-                const uint32_t sfa = tmem + kStreamRows + (uint32_t)(g & 1) * 2 * Cfg::kScaleCols, sfb = sfa + Cfg::kScaleCols;
-                if (g + 1 < nk) issue_stage<NV, false, 1>(lead, tmem, a0, b0, s0, s0 + Cfg::kS, sfa, sfb, 0u, idesc, g == 0, kStepTiles<NV>, 4);
-                else issue_stage<NV, false, 1>(lead, tmem, a0, b0, s0, s0 + Cfg::kS, sfa, sfb, 0u, idesc, g == 0, tail_tiles, tail_ks);
+                issue_scales<NV, false, 1>(lead, s0, s0 + Cfg::kS, sfa, sfb);
+                issue_mmas<NV, false, 1>(lead, tmem, a0, b0, sfa, sfb, 0u, idesc, g == 0);
                 commit<false>(lead, empty + 8 * s);
                 if (++s == stages) {
                     s = 0;
@@ -391,14 +428,14 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         float scale = 1.0f;
         if (p.ts_a) scale = __fmul_rn(scale, *p.ts_a);
         if (p.ts_w) scale = __fmul_rn(scale, p.ts_w[ue]);
-        const int64_t ldy = p.gate ? p.N / 2 : p.N;
+        const int64_t ldy = GATE ? p.N / 2 : p.N;
         if (mbar_wait_warp(acc_full, 0, abort_flag)) {
             tc_fence_after();
 #pragma unroll 1
             for (int c0 = 0; c0 < count; c0 += 32) {
                 float v[32];
                 tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0, v);
-write_columns<TOut>(v, scale, p, Y, ldy, row0 + c0, count - c0, n, lane);
+write_columns<TOut, GATE>(v, scale, p.N, Y, ldy, row0 + c0, count - c0, n, lane);
             }
         }
         tc_fence_before();
@@ -419,16 +456,18 @@ write_columns<TOut>(v, scale, p, Y, ldy, row0 + c0, count - c0, n, lane);
 // rows is what the FP4 rate asks for: an SM's operands per 256 k are (128 +
 // 96) x 128 bytes for 384 cycles of MMA, 75 bytes a cycle, where one CTA
 // alone would need 107.
-//   warp 0: bulk-tensor producer (each CTA loads its own operands; the
-//   leader's barrier counts both); warp 1: tensor memory, and in the leader
-//   the MMA issuer; warps 2-5: epilogue, a quarter of the lanes each.
+//   warps 0 and 10: bulk-tensor producers, weights and activations (each CTA
+//   loads its own operands; the leader's barrier counts both); one warp alone
+//   needs 390 cycles for a stage's four copies, as long as its MMAs take;
+//   warp 1: tensor memory, and in the leader the MMA issuer;
+//   warps 2-9: epilogue, two warps per quarter of the lanes.
 // Two accumulators of 192 columns: the epilogue of a unit runs beside the MMAs
-// of the next.  384 + 2 x 24 (NVFP4: 2 x 48) columns of scales fit in 512;
-// 256-wide accumulators would leave no room for them.
+// of the next.  384 + 24 (NVFP4: 48) columns of scales fit in 512; 256-wide
+// accumulators would leave no room for them.
 // A unit's rows start at a multiple of 64 rows of their group, so its scales
 // start at column 0 or 2 of their tile.
 // ---------------------------------------------------------------------------
-constexpr int kPairRows = 192, kPairThreads = 192;
+constexpr int kPairRows = 192, kPairEpiWarps = 8, kPairThreads = 96 + 32 * kPairEpiWarps;
 
 template <bool NV> struct PairCfg {
     static constexpr uint32_t kA = 128 * 128, kB = kPairRows / 2 * 128, kS = kStepTiles<NV> * kTileBytes;
@@ -436,7 +475,7 @@ template <bool NV> struct PairCfg {
     static constexpr int kStages = (int)((232448u - 1024u - 512u) / kStage);
     static constexpr uint32_t kSmem = kStages * kStage + 512u + 1024u;
     static constexpr uint32_t kSfaCols = kStepTiles<NV> * 4, kSfbCols = kStepTiles<NV> * 8;
-    static_assert(2 * kPairRows + 2 * (kSfaCols + kSfbCols) <= 512, "tensor memory");
+    static_assert(2 * kPairRows + kSfaCols + kSfbCols <= 512, "tensor memory");
     static_assert(16 * kStages + 40 <= 256, "barriers");
 };
 
@@ -462,28 +501,22 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // loads into this CTA's shared memory that count on a barrier of either CTA of the pair
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t lead, uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar)
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar)
 {
     asm volatile(
-        "{ .reg .pred e; setp.ne.b32 e, %5, 0;\n"
-        "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4]; }" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "r"(lead)
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t lead, uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar)
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar)
 {
     asm volatile(
-        "{ .reg .pred e; setp.ne.b32 e, %6, 0;\n"
-        "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5]; }" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "r"(lead)
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void mbar_expect_tx_one(uint32_t lead, uint32_t bar, uint32_t bytes)
-{
-    asm volatile("{ .reg .pred e; setp.ne.b32 e, %2, 0; @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1; }" ::"r"(bar), "r"(bytes), "r"(lead)
-                 : "memory");
-}
-template <bool NV, typename TOut>
+
+template <bool NV, typename TOut, bool GATE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a,
                    const __grid_constant__ CUtensorMap tmap_sw, const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ Problem p,
@@ -509,7 +542,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(acc_full + 8 * b, 1);
-            mbar_init(acc_empty + 8 * b, 8);  // the epilogue warps of both CTAs
+            mbar_init(acc_empty + 8 * b, 2 * kPairEpiWarps);  // the epilogue warps of both CTAs
         }
         mbar_init(drained, 1);
         *abort_flag = 0;
@@ -528,8 +561,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (p.E > 0 && blockIdx.x == 0) check_offsets(p.offsets, p.E, p.T);
     const int nk = (p.K + kStepK - 1) / kStepK;
 
-    if (warp == 0) {
-        // ---------------- producer ----------------
+    if (warp == 0 || warp == kPairEpiWarps + 2) {
+        // ---------------- producers ----------------
         const uint32_t lead = elect_one(), full0 = cluster_addr(full, 0);
         uint32_t s = 0, ph = 0;
         bool ok = true, first = true;
@@ -549,13 +582,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 // fault injection (tests only): the first CTA never fills its first stage
                 const bool stall = inject_stall && blockIdx.x == 0 && first;
                 first = false;
-                if (!stall) {
-                    const uint32_t a0 = smem_addr(smem) + s * Cfg::kStage, f = full0 + 8 * s, s0 = a0 + Cfg::kA + Cfg::kB;
-                    if (rank == 0) mbar_expect_tx_one(lead, full + 8 * s, 2 * Cfg::kStage);
-                    tma_load_2d_pair(lead, a0, &tmap_w, g * 128, wrow, f);
-                    tma_load_2d_pair(lead, a0 + Cfg::kA, &tmap_a, g * 128, arow, f);
-                    tma_load_3d_pair(lead, s0, &tmap_sw, 0, g * kStepTiles<NV> * 2, srow, f);
-                    tma_load_3d_pair(lead, s0 + Cfg::kS, &tmap_sa, 0, g * kStepTiles<NV> * 2, w.trow, f);
+                const uint32_t a0 = smem_addr(smem) + s * Cfg::kStage, f = full0 + 8 * s, s0 = a0 + Cfg::kA + Cfg::kB;
+                const int t0 = g * kStepTiles<NV> * 2;
+                if (lead && !stall) {
+                    if (warp == 0) {
+                        if (rank == 0) mbar_expect_tx(full + 8 * s, 2 * Cfg::kStage);
+                        tma_load_2d_pair(a0, &tmap_w, g * 128, wrow, f);
+                        tma_load_3d_pair(s0, &tmap_sw, 0, t0, srow, f);
+                    } else {
+                        tma_load_2d_pair(a0 + Cfg::kA, &tmap_a, g * 128, arow, f);
+                        tma_load_3d_pair(s0 + Cfg::kS, &tmap_sa, 0, t0, w.trow, f);
+                    }
                 }
                 if (++s == STAGES) {
                     s = 0;
@@ -573,8 +610,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     } else if (warp == 1) {
         if (rank == 0) {
             // ---------------- MMA issuer (leader) ----------------
-            const uint32_t lead = elect_one();
-            const int tail_tiles = p.ct - (nk - 1) * kStepTiles<NV>, tail_ks = (p.K - (nk - 1) * kStepK + 63) / 64;
+            const uint32_t lead = elect_one(), sfa = tmem + 2 * kPairRows, sfb = sfa + Cfg::kSfaCols;
+            // One stage's copies, then its MMAs, the scales always in the same columns
+            // (copies and MMAs of one thread run in order).  The tensor pipe is the
+            // bound: 445 cycles a stage for MXFP4 with loads left out, 478 for NVFP4,
+            // 384 of them MMAs.  Copying the next stage's scales between the MMAs of
+            // this one, or two stages' at once, measured 10% slower.
             uint32_t s = 0, ph = 0, ti = 0;
             bool ok = true;
             for (int u = pair; ok; u += pairs, ti++) {
@@ -583,7 +624,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const uint32_t b = ti & 1u, acc = tmem + b * kPairRows;
                 // the epilogue has drained this accumulator
                 if (!mbar_wait_all(acc_empty + 8 * b, ((ti >> 1) & 1u) ^ 1u, abort_flag)) break;
-                tc_fence_after();
                 const uint32_t idesc = idesc_fp4(NV, 256, (w.count + 15) & ~15), off2 = (uint32_t)w.off >> 5;
                 for (int g = 0; g < nk; g++) {
                     if (!mbar_wait_all(full + 8 * s, ph, abort_flag)) {
@@ -592,11 +632,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     }
                     tc_fence_after();
                     const uint32_t a0 = smem_addr(smem) + s * Cfg::kStage, b0 = a0 + Cfg::kA, s0 = b0 + Cfg::kB;
-                    const uint32_t sfa = tmem + 2 * kPairRows + (uint32_t)(g & 1) * (Cfg::kSfaCols + Cfg::kSfbCols), sfb = sfa + Cfg::kSfaCols;
-                    if (g + 1 < nk)
-                        issue_stage<NV, true, 2>(lead, acc, a0, b0, s0, s0 + Cfg::kS, sfa, sfb, off2, idesc, g == 0, kStepTiles<NV>, 4);
-                    else
-                        issue_stage<NV, true, 2>(lead, acc, a0, b0, s0, s0 + Cfg::kS, sfa, sfb, off2, idesc, g == 0, tail_tiles, tail_ks);
+                    issue_scales<NV, true, 2>(lead, s0, s0 + Cfg::kS, sfa, sfb);
+                    issue_mmas<NV, true, 2>(lead, acc, a0, b0, sfa, sfb, off2, idesc, g == 0);
                     commit<true>(lead, empty + 8 * s);
                     if (++s == STAGES) {
                         s = 0;
@@ -617,9 +654,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
     } else {
         // ---------------- epilogue ----------------
-        const int q = warp & 3;
+        const int q = warp & 3, c_first = ((warp - 2) >> 2) * 32;  // quarter of the lanes; which of each 64 columns
         const uint32_t acc_empty0 = cluster_addr(acc_empty, 0);
-        const int64_t ldy = p.gate ? p.N / 2 : p.N;
+        const int64_t ldy = GATE ? p.N / 2 : p.N;
         const float ts_a = p.ts_a ? *p.ts_a : 1.0f;
         uint32_t ti = 0;
         for (int u = pair;; u += pairs, ti++) {
@@ -631,16 +668,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int n = (u % ntiles) * 256 + (int)rank * 128 + q * 32 + lane;
             const float scale = p.ts_w ? __fmul_rn(ts_a, p.ts_w[w.e]) : ts_a;
 #pragma unroll 1
-            for (int c0 = 0; c0 < w.count; c0 += 32) {
+            for (int c0 = c_first; c0 < w.count || c0 == c_first; c0 += 64) {
                 float v[32];
                 tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + b * kPairRows + (uint32_t)c0, v);
-                if (c0 + 32 >= w.count) {
-                    // this warp has read the whole accumulator: hand it back
+                if (c0 + 64 >= w.count) {
+                    // this warp has read its part of the accumulator: hand it back
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8 * b);
                 }
-                write_columns<TOut>(v, scale, p, Y, ldy, w.row0 + c0, w.count - c0, n, lane);
+                write_columns<TOut, GATE>(v, scale, p.N, Y, ldy, w.row0 + c0, w.count - c0, n, lane);
             }
         }
         tc_fence_before();
@@ -692,31 +729,35 @@ static bool encode_tiles_map(CUtensorMap *map, const void *base, int64_t trows, 
 // pieces of `step` rows that T rows in E groups can make
 static int64_t max_pieces(int64_t T, int64_t E, int64_t step) { return E == 0 ? (T + step - 1) / step : T / step + (E < T ? E : T); }
 
-template <bool NV, typename TOut>
+template <bool NV, typename TOut, bool GATE>
 static razer_status launch_stream(const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, TOut *Y, cudaStream_t st)
 {
     static bool attr_set[64] = {false};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        if (cudaFuncSetAttribute(mx_stream_kernel<NV, TOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStreamSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(mx_stream_kernel<NV, TOut, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStreamSmem) != cudaSuccess)
             return RAZER_ERR_CUDA;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    CUtensorMap mw, ma;
-    if (!encode_codes_map(&mw, codes_w, (int64_t)p.N * (p.E ? p.E : 1), p.K, 128) || !encode_codes_map(&ma, codes_a, p.T, p.K, kBoxRows))
+    CUtensorMap mw, ma, msw, msa;
+    const int64_t E = p.E ? p.E : 1, arows = p.E ? tile_rows_grouped(p.T, p.E) : tile_rows(p.T);
+    if (!encode_codes_map(&mw, codes_w, p.N * E, p.K, 128) || !encode_codes_map(&ma, codes_a, p.T, p.K, kBoxRows) ||
+        !encode_tiles_map(&msw, p.tiles_w, E * p.trows_w, p.ct, 1, kStepTiles<NV>) ||
+        !encode_tiles_map(&msa, p.tiles_a, arows, p.ct, 1, kStepTiles<NV>))
         return RAZER_ERR_CUDA;
     const int ntiles = (p.N + 127) / 128;
     const int64_t grid = max_pieces(p.T, p.E, kStreamRows) * ntiles;
     if (grid > INT32_MAX) return RAZER_ERR_SHAPE;
     const int inject = fault_injection_enabled() ? 1 : 0;
-    if (launch_pdl(mx_stream_kernel<NV, TOut>, (unsigned)grid, (unsigned)kStreamThreads, (size_t)kStreamSmem, st, mw, ma, p, ntiles, Y,
+    if (launch_pdl(mx_stream_kernel<NV, TOut, GATE>, (unsigned)grid, (unsigned)kStreamThreads, (size_t)kStreamSmem, st, mw, ma, msw, msa, p,
+                   ntiles, Y,
                    inject) != cudaSuccess)
         return RAZER_ERR_CUDA;
     return RAZER_OK;
 }
 
-template <bool NV, typename TOut>
+template <bool NV, typename TOut, bool GATE>
 static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, int step, TOut *Y, cudaStream_t st)
 {
     using Cfg = PairCfg<NV>;
@@ -725,7 +766,7 @@ static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, 
     cudaGetDevice(&dev);
     int pairs = dev >= 0 && dev < 64 ? resident[dev] : 0;
     if (pairs == 0) {
-        if (cudaFuncSetAttribute(mx_pair_kernel<NV, TOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(mx_pair_kernel<NV, TOut, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmem) != cudaSuccess)
             return RAZER_ERR_CUDA;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(sm_count() & ~1));
@@ -737,7 +778,7 @@ static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, 
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&pairs, mx_pair_kernel<NV, TOut>, &cfg) != cudaSuccess || pairs < 1) return RAZER_ERR_CUDA;
+        if (cudaOccupancyMaxActiveClusters(&pairs, mx_pair_kernel<NV, TOut, GATE>, &cfg) != cudaSuccess || pairs < 1) return RAZER_ERR_CUDA;
         pairs = std::min(pairs, sm_count() / 2);
         if (dev >= 0 && dev < 64) resident[dev] = pairs;
     }
@@ -751,18 +792,18 @@ static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, 
     const int64_t units = max_pieces(p.T, p.E, step) * ntiles;
     if (units > INT32_MAX - 1024) return RAZER_ERR_SHAPE;
     const int inject = fault_injection_enabled() ? 1 : 0;
-    if (launch_pdl(mx_pair_kernel<NV, TOut>, 2u * (unsigned)std::min<int64_t>(units, pairs), (unsigned)kPairThreads, (size_t)Cfg::kSmem, st, mw,
+    if (launch_pdl(mx_pair_kernel<NV, TOut, GATE>, 2u * (unsigned)std::min<int64_t>(units, pairs), (unsigned)kPairThreads, (size_t)Cfg::kSmem, st, mw,
                    ma, msw, msa, p, ntiles, step, Y, inject) != cudaSuccess)
         return RAZER_ERR_CUDA;
     return RAZER_OK;
 }
 
-template <bool NV, typename TOut>
+template <bool NV, typename TOut, bool GATE>
 static razer_status launch_mx(const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, TOut *Y, cudaStream_t st)
 {
     const int64_t rows = p.E > 0 ? (p.T + p.E - 1) / p.E : p.T;  // rows of a group, on average
-    if (rows > 64) return launch_pair<NV, TOut>(codes_a, codes_w, p, kPairRows, Y, st);
-    return launch_stream<NV, TOut>(codes_a, codes_w, p, Y, st);
+    if (rows > 64) return launch_pair<NV, TOut, GATE>(codes_a, codes_w, p, kPairRows, Y, st);
+    return launch_stream<NV, TOut, GATE>(codes_a, codes_w, p, Y, st);
 }
 
 template <typename TOut>
@@ -773,7 +814,8 @@ static razer_status run_mx_t(bool nv, const uint8_t *codes_a, const uint8_t *cod
         mx_zero_kernel<TOut><<<sm_count() * 4, 256, 0, st>>>(p.offsets, p.E, p.T, cols, Y);
         return last_launch_status();
     }
-    return nv ? launch_mx<true, TOut>(codes_a, codes_w, p, Y, st) : launch_mx<false, TOut>(codes_a, codes_w, p, Y, st);
+    if (p.gate) return nv ? launch_mx<true, TOut, true>(codes_a, codes_w, p, Y, st) : launch_mx<false, TOut, true>(codes_a, codes_w, p, Y, st);
+    return nv ? launch_mx<true, TOut, false>(codes_a, codes_w, p, Y, st) : launch_mx<false, TOut, false>(codes_a, codes_w, p, Y, st);
 }
 
 }  // namespace mx
