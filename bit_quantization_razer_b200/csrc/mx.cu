@@ -43,6 +43,40 @@ __device__ __forceinline__ unsigned e2m1x8(const float (&v)[8])
     return r;
 }
 
+// The scale byte of a block whose largest magnitude has the 16-bit pattern m,
+// and 2^-e as a binary32
+template <typename T> __device__ __forceinline__ unsigned scale_byte(unsigned m, float &inv)
+{
+    const unsigned field = __float_as_uint(Abs16<T>::to_f(m)) >> 23;  // binary32 exponent field
+    const unsigned byte = m >= Abs16<T>::kInf ? 255u : (field > 2u ? field - 2u : 0u);
+    inv = __uint_as_float((254u - (byte == 255u ? 0u : byte)) << 23);
+    return byte;
+}
+__device__ __forceinline__ unsigned abs_max2(uint4 v)
+{
+    return __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+}
+template <typename T> __device__ __forceinline__ unsigned encode8(uint4 v, float inv)
+{
+    const float2 a = In16<T>::to_f2(v.x), b = In16<T>::to_f2(v.y), c = In16<T>::to_f2(v.z), d = In16<T>::to_f2(v.w);
+    const float s[8] = {a.x * inv, a.y * inv, b.x * inv, b.y * inv, c.x * inv, c.y * inv, d.x * inv, d.y * inv};
+    return e2m1x8(s);
+}
+
+// One thread's block of 32: its codes, and the scale byte as the result
+template <typename T> __device__ __forceinline__ unsigned quantize_block(const T *__restrict__ x, uint4 &codes)
+{
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[i] = __ldg(reinterpret_cast<const uint4 *>(x) + i);
+    const unsigned m2 = __vmaxu2(__vmaxu2(abs_max2(v[0]), abs_max2(v[1])), __vmaxu2(abs_max2(v[2]), abs_max2(v[3])));
+    float inv;
+    const unsigned byte = scale_byte<T>(max(m2 & 0xFFFFu, m2 >> 16), inv);
+    codes = make_uint4(encode8<T>(v[0], inv), encode8<T>(v[1], inv), encode8<T>(v[2], inv), encode8<T>(v[3], inv));
+    if (byte == 255u) codes = make_uint4(0u, 0u, 0u, 0u);
+    return byte;
+}
+
 constexpr int kVecs = 4;            // 16-byte vectors per lane and task
 constexpr int kTaskCols = 256 * kVecs;
 
@@ -85,16 +119,12 @@ __global__ void __launch_bounds__(256) quantize_mx_kernel(const T *__restrict__ 
         for (int i = 0; i < kVecs; i++) {
             if ((task - r * chunks) * kTaskCols + 256 * i >= K) break;  // the same for the whole warp
             const int64_t c = c0 + 256 * i;
-            unsigned m2 = __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu), __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+            unsigned m2 = abs_max2(v[i]);
             m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
             m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 2));
-            const unsigned m = max(m2 & 0xFFFFu, m2 >> 16);
-            const unsigned field = __float_as_uint(Abs16<T>::to_f(m)) >> 23;  // binary32 exponent field of the block's largest magnitude
-            const unsigned byte = m >= Abs16<T>::kInf ? 255u : (field > 2u ? field - 2u : 0u);
-            const float inv = __uint_as_float((254u - (byte == 255u ? 0u : byte)) << 23);
-            const float2 a = In16<T>::to_f2(v[i].x), b = In16<T>::to_f2(v[i].y), d = In16<T>::to_f2(v[i].z), f = In16<T>::to_f2(v[i].w);
-            const float s[8] = {a.x * inv, a.y * inv, b.x * inv, b.y * inv, d.x * inv, d.y * inv, f.x * inv, f.y * inv};
-            if (c < K) *reinterpret_cast<unsigned *>(codes + (r * K + c) / 2) = byte == 255u ? 0u : e2m1x8(s);
+            float inv;
+            const unsigned byte = scale_byte<T>(max(m2 & 0xFFFFu, m2 >> 16), inv);
+            if (c < K) *reinterpret_cast<unsigned *>(codes + (r * K + c) / 2) = byte == 255u ? 0u : encode8<T>(v[i], inv);
             // a word holds the scales of 4 blocks: 16 lanes; blocks past K give 0
             unsigned w = c < K ? byte << (8 * ((lane >> 2) & 3)) : 0u;
             w |= __shfl_xor_sync(0xffffffffu, w, 4);

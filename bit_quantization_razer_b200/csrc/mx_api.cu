@@ -10,7 +10,8 @@ razer_status run_dequant_mx(const uint8_t *codes, const uint8_t *tiles, int64_t 
                             razer_dtype dt, cudaStream_t st);
 razer_status run_tile_scales(const uint8_t *rows, int64_t batch, int64_t R, int64_t C, const int32_t *offsets, int E, uint8_t *tiles,
                              cudaStream_t st);
-razer_status run_gemm_mx(const uint8_t *codes_a, const uint8_t *tiles_a, const float *ts_a, int64_t T, const int32_t *offsets, int E,
+bool gemm_mx_fuses(int64_t T, int64_t E);
+razer_status run_gemm_mx(const void *X, razer_dtype x_dt, const uint8_t *codes_a, const uint8_t *tiles_a, const float *ts_a, int64_t T, const int32_t *offsets, int E,
                          const uint8_t *codes_w, const uint8_t *tiles_w, const float *ts_w, razer_format fmt, int64_t N, int64_t K, int gate,
                          void *Y, razer_dtype out_dt, cudaStream_t st);
 
@@ -49,7 +50,7 @@ static size_t mx_tiles_bytes(bool nv, int64_t T, int64_t K, int64_t E)
 
 size_t gemm_mx_online_workspace_bytes(int64_t T, int64_t K, int64_t E)
 {
-    if (T <= 0 || K <= 0 || E < 0) return 0;
+    if (T <= 0 || K <= 0 || E < 0 || gemm_mx_fuses(T, E)) return 0;
     return packed_bytes(T, K) + mx_tiles_bytes(false, T, K, E);
 }
 
@@ -66,7 +67,7 @@ static razer_status gemm_mx_checked(const uint8_t *codes_a, const uint8_t *scale
     // NVFP4 values are code * scale * ts: without ts the call is incomplete
     if (fmt == RAZER_FMT_NVFP4 && (!ts_a || !ts_w)) return RAZER_ERR_INVALID_ARG;
     if (T == 0 || N == 0) return RAZER_OK;
-    return run_gemm_mx(codes_a, scales_a, ts_a, T, offsets, (int)E, codes_w, scales_w, ts_w, fmt, N, K, act == RAZER_ACT_SILU_MUL ? 1 : 0, Y,
+    return run_gemm_mx(nullptr, RAZER_BF16, codes_a, scales_a, ts_a, T, offsets, (int)E, codes_w, scales_w, ts_w, fmt, N, K, act == RAZER_ACT_SILU_MUL ? 1 : 0, Y,
                        out_dt, st);
 }
 
@@ -87,10 +88,14 @@ static razer_status gemm_mx_online_checked(const void *X, razer_dtype x_dt, int6
         if (!workspace || ws_bytes < need) return RAZER_ERR_WORKSPACE;
         if (!aligned(workspace, 16)) return RAZER_ERR_ALIGN;
     }
+    const int gate = act == RAZER_ACT_SILU_MUL ? 1 : 0;
+    if (gemm_mx_fuses(T, E))
+        return run_gemm_mx(X, x_dt, nullptr, nullptr, nullptr, T, offsets, (int)E, codes_w, scales_w, nullptr, RAZER_FMT_MXFP4, N, K, gate, Y, out_dt,
+                           st);
     uint8_t *codes_a = reinterpret_cast<uint8_t *>(workspace), *scales_a = codes_a + packed_bytes(T, K);
     if (K > 0 && (s = run_quantize_mx(X, x_dt, T, K, offsets, (int)E, codes_a, scales_a, st)) != RAZER_OK) return s;
-    return run_gemm_mx(codes_a, scales_a, nullptr, T, offsets, (int)E, codes_w, scales_w, nullptr, RAZER_FMT_MXFP4, N, K,
-                       act == RAZER_ACT_SILU_MUL ? 1 : 0, Y, out_dt, st);
+    return run_gemm_mx(nullptr, x_dt, codes_a, scales_a, nullptr, T, offsets, (int)E, codes_w, scales_w, nullptr, RAZER_FMT_MXFP4, N, K, gate, Y,
+                       out_dt, st);
 }
 
 }  // namespace razer

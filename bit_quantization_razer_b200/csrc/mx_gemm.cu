@@ -18,6 +18,7 @@
 // RAZER_ERR_TIMEOUT, the other roles stop at their next wait, copies in
 // flight are waited for (bounded) and the tensor memory is freed.
 #include <algorithm>
+#include <type_traits>
 
 #include "mx.cuh"
 #include "sm100_async.cuh"
@@ -272,6 +273,30 @@ __device__ __forceinline__ void write_columns(const float (&v)[32], float scale,
     }
 }
 
+// shared-memory address of the same object in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 // ---------------------------------------------------------------------------
 // mx_stream_kernel: few rows per group.  One CTA per 128 weight rows x up to
 // 128 activation rows: its time is the weights' way from HBM, so the ring of
@@ -279,13 +304,21 @@ __device__ __forceinline__ void write_columns(const float (&v)[32], float scale,
 // activation rows (in boxes of 32) as the unit has, so that few rows leave
 // room for more stages (5 of 22 KB for up to 32 rows, 3 of 34 KB for 128).
 //   warp 0: bulk-tensor producer; warp 1: tensor memory, MMA issuer;
-//   warps 2-5: epilogue, one quarter of the accumulator's lanes each.
+//   warps 2-9: with TIn = void the epilogue alone, two warps per quarter of the
+//   accumulator's lanes; otherwise they first quantize the activations (TIn
+//   [T, K]) to MXFP4, stage by stage, straight into the shared-memory operand
+//   and its scale tiles: a call with few rows is then one launch, reads X from
+//   L2 and needs no workspace.
 // Stage: 256 k of 128 weight rows (16 KB) and of the activation rows, and the
 // scale tiles of both.
+// Where the units do not fill the SMs, the CTAs of a cluster share one: CTA z
+// takes part z of K, leaves its fp32 sums in its own shared memory, and after
+// a cluster barrier each CTA adds a share of the columns over the CTAs in
+// order (deterministic; no workspace, no second launch).
 // ---------------------------------------------------------------------------
-constexpr int kStreamThreads = 192;
+constexpr int kStreamWorkers = 8, kStreamThreads = 64 + 32 * kStreamWorkers;
 
-constexpr int kStreamRows = 128, kBoxRows = 32;
+constexpr int kStreamRows = 128, kBoxRows = 32, kFuseRows = 16;
 // two CTAs per SM: 227 KB / 2 less 1 KB each that the system keeps
 constexpr uint32_t kStreamRing = 115200u - 1024u - 512u, kStreamSmem = kStreamRing + 512u + 1024u;
 constexpr int kStreamMaxStages = 8;
@@ -296,17 +329,20 @@ template <bool NV> struct StreamCfg {
     static constexpr uint32_t kScaleCols = kStepTiles<NV> * 4;
     static constexpr uint32_t kCols = 256;
     static_assert(kStreamRows + 2 * kScaleCols <= kCols, "two CTAs share an SM's tensor memory");
-    static_assert(kStreamRing / (kA + kBox + 2 * kS) <= kStreamMaxStages, "barriers for every stage");
+    static_assert(kStreamRing / (kA + kBox + 2 * kS) <= kStreamMaxStages && kStreamMaxStages <= kStreamWorkers, "barriers and a warp for every stage");
     static_assert(kStreamRing / (kA + kStreamRows * 128 + 2 * kS) >= 3, "a ring for the widest unit");
 };
+static_assert(kStreamRows * 128 * 4 <= kStreamRing, "the sums of a cluster's CTA");
 
-template <bool NV, typename TOut, bool GATE>
+template <bool NV, typename TOut, bool GATE, typename TIn>
 __global__ void __launch_bounds__(kStreamThreads, 2)
     mx_stream_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a,
                      const __grid_constant__ CUtensorMap tmap_sw, const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ Problem p,
-                     int ntiles, TOut *__restrict__ Y, int inject_stall)
+                     const TIn *__restrict__ X, int ntiles, int splits, TOut *__restrict__ Y, int inject_stall)
 {
     using Cfg = StreamCfg<NV>;
+    constexpr bool kFused = !std::is_void<TIn>::value;
+    static_assert(!(kFused && NV), "the quantizer writes MXFP4");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *bars = smem + kStreamRing;
@@ -315,11 +351,12 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 260);
     volatile int *unit_slot = reinterpret_cast<volatile int *>(bars + 264);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n0 = (int)(blockIdx.x % (unsigned)ntiles) * 128, t = (int)(blockIdx.x / (unsigned)ntiles);
+    const int z = splits > 1 ? (int)cluster_rank() : 0, block = blockIdx.x / (unsigned)splits;
+    const int n0 = block % ntiles * 128, t = block / ntiles;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStreamMaxStages; s++) {
-            mbar_init(full + 8 * s, 1);
+            mbar_init(full + 8 * s, kFused ? 2 : 1);  // the producer, and the warp that quantizes the stage
             mbar_init(empty + 8 * s, 1);
         }
         mbar_init(acc_full, 1);
@@ -332,7 +369,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
                      "n"(Cfg::kCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    pdl_wait();  // the activations come from an earlier kernel of the stream
+    pdl_wait();  // the operands may come from an earlier kernel of the stream
     if (p.E > 0 && blockIdx.x == 0) check_offsets(p.offsets, p.E, p.T);
     if (warp == 0) {
         const RowUnit u = row_unit(p, t, kStreamRows);
@@ -348,7 +385,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int ue = unit_slot[0], row0 = unit_slot[1], count = unit_slot[2], trow = unit_slot[3];
-    const int nk = count > 0 ? (p.K + kStepK - 1) / kStepK : 0;
+    // this CTA's stages g0 .. g0 + nk - 1
+    const int steps = (p.K + kStepK - 1) / kStepK;
+    const int g0 = (int)((int64_t)steps * z / splits), nk = count > 0 ? (int)((int64_t)steps * (z + 1) / splits) - g0 : 0;
     const int boxes = (count + kBoxRows - 1) / kBoxRows;
     const uint32_t bbytes = (uint32_t)boxes * Cfg::kBox, stage = Cfg::kA + bbytes + 2 * Cfg::kS;
     const uint32_t stages = kStreamRing / stage;
@@ -368,12 +407,15 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             // fault injection (tests only): the first CTA never fills its first stage
             const bool stall = inject_stall && blockIdx.x == 0 && g == 0;
             const uint32_t a0 = smem_addr(smem) + s * stage, f = full + 8 * s, s0 = a0 + Cfg::kA + bbytes;
+            const int c0 = (g0 + g) * 128, t0 = (g0 + g) * kStepTiles<NV> * 2;
             if (lead && !stall) {
-                mbar_expect_tx(f, stage);
-                tma_load_2d(a0, &tmap_w, g * 128, wrow, f);
-                tma_load_3d(s0, &tmap_sw, 0, g * kStepTiles<NV> * 2, srow, f);
-                for (int b = 0; b < boxes; b++) tma_load_2d(a0 + Cfg::kA + b * Cfg::kBox, &tmap_a, g * 128, row0 + b * kBoxRows, f);
-                tma_load_3d(s0 + Cfg::kS, &tmap_sa, 0, g * kStepTiles<NV> * 2, trow, f);
+                mbar_expect_tx(f, kFused ? Cfg::kA + Cfg::kS : stage);
+                tma_load_2d(a0, &tmap_w, c0, wrow, f);
+                tma_load_3d(s0, &tmap_sw, 0, t0, srow, f);
+                if constexpr (!kFused) {
+                    for (int b = 0; b < boxes; b++) tma_load_2d(a0 + Cfg::kA + b * Cfg::kBox, &tmap_a, c0, row0 + b * kBoxRows, f);
+                    tma_load_3d(s0 + Cfg::kS, &tmap_sa, 0, t0, trow, f);
+                }
             }
             if (++s == stages) {
                 s = 0;
@@ -381,12 +423,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             }
         }
         if (!ok) {
-            // let the loads already issued land before the CTA exits (bounded)
+            // loads already issued land within microseconds; their barriers may
+            // never complete: wait a fixed 2 ms before the CTA exits
             const uint64_t t0 = globaltimer();
-            for (int gg = g > (int)stages ? g - (int)stages : 0; gg < g; gg++) {
-                if (inject_stall && blockIdx.x == 0 && gg == 0) continue;
-                while (!mbar_try_wait(full + 8 * ((uint32_t)gg % stages), ((uint32_t)gg / stages) & 1u) && globaltimer() - t0 < kTimeoutNs) {
-                }
+            while (globaltimer() - t0 < 2000000ull) {
             }
             __syncwarp();
         }
@@ -421,21 +461,56 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             }
             __syncwarp();
         }
-    } else if (count > 0) {
+    } else {
+        bool ok = true;
+        if constexpr (kFused) {
+            // ---------------- quantizer: a warp for each place of the ring ----------------
+            // (a warp that went on to another place could be two rounds ahead of it,
+            // which a barrier's parity cannot tell from none)
+            const uint32_t s = (uint32_t)warp - 2;
+            uint32_t ph = 0;
+            for (int g = (int)s; g < nk && s < stages; g += (int)stages, ph ^= 1u) {
+                if (!mbar_wait_all(empty + 8 * s, ph ^ 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *b0 = smem + s * stage + Cfg::kA, *sb = b0 + bbytes + Cfg::kS;
+                const int k0 = (g0 + g) * kStepK;
+                // 8 blocks a row: a block's 16 bytes of codes are one unit of the swizzle
+                for (int i = lane; i < count * 8; i += 32) {
+                    const int r = i >> 3, c = i & 7;
+                    uint4 codes = make_uint4(0u, 0u, 0u, 0u);
+                    unsigned byte = 0u;
+                    if (k0 + 32 * c < p.K) byte = quantize_block<TIn>(X + (int64_t)(row0 + r) * p.K + k0 + 32 * c, codes);
+                    *reinterpret_cast<uint4 *>(b0 + r * 128 + ((c ^ (r & 7)) << 4)) = codes;
+                    sb[(c >> 2) * kTileBytes + (r & 31) * 16 + (r >> 5) * 4 + (c & 3)] = (uint8_t)byte;
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full + 8 * s);
+            }
+        }
         // ---------------- epilogue ----------------
-        const int q = warp & 3;  // the quarter of the lanes this warp may read
-        const int n = n0 + q * 32 + lane;
-        float scale = 1.0f;
-        if (p.ts_a) scale = __fmul_rn(scale, *p.ts_a);
-        if (p.ts_w) scale = __fmul_rn(scale, p.ts_w[ue]);
-        const int64_t ldy = GATE ? p.N / 2 : p.N;
-        if (mbar_wait_warp(acc_full, 0, abort_flag)) {
+        if (nk > 0 && ok && mbar_wait_warp(acc_full, 0, abort_flag)) {
             tc_fence_after();
+            const int q = warp & 3, r = q * 32 + lane;  // the quarter of the lanes this warp may read
+            float scale = 1.0f;
+            if (p.ts_a) scale = __fmul_rn(scale, *p.ts_a);
+            if (p.ts_w) scale = __fmul_rn(scale, p.ts_w[ue]);
+            const int64_t ldy = GATE ? p.N / 2 : p.N;
 #pragma unroll 1
-            for (int c0 = 0; c0 < count; c0 += 32) {
+            for (int c0 = ((warp - 2) >> 2) * 32; c0 < count; c0 += 64) {
                 float v[32];
                 tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0, v);
-write_columns<TOut, GATE>(v, scale, p.N, Y, ldy, row0 + c0, count - c0, n, lane);
+                if (splits == 1) {
+                    write_columns<TOut, GATE>(v, scale, p.N, Y, ldy, row0 + c0, count - c0, n0 + r, lane);
+                } else {
+                    // the ring is free: every stage has been read by the MMAs
+                    float *part = reinterpret_cast<float *>(smem) + c0 * 128 + r;
+#pragma unroll
+                    for (int i = 0; i < 32; i++)
+                        if (c0 + i < count) part[i * 128] = v[i] * scale;
+                }
             }
         }
         tc_fence_before();
@@ -445,6 +520,26 @@ write_columns<TOut, GATE>(v, scale, p.N, Y, ldy, row0 + c0, count - c0, n, lane)
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(Cfg::kCols));
+    }
+    if (splits > 1) {
+        cluster_sync();  // every CTA's sums are written
+        if (warp >= 2 && count > 0) {
+            const int w = warp - 2, q = w & 3, n = n0 + q * 32 + lane;
+            const int64_t ldy = GATE ? p.N / 2 : p.N;
+            for (int c = z * 2 + (w >> 2); c < count; c += 2 * splits) {
+                const uint32_t at = smem_addr(smem) + (uint32_t)(c * 128 + q * 32 + lane) * 4u;
+                float a = 0.0f;
+                for (int y = 0; y < splits; y++) a += ld_cluster(cluster_addr(at, (uint32_t)y));
+                if constexpr (GATE) {
+                    const float up = __shfl_xor_sync(0xffffffffu, a, 1);
+                    if (n < p.N && !(lane & 1)) store1<TOut>(Y + (int64_t)(row0 + c) * ldy + n / 2, silu_mul(a, up));
+                } else {
+                    if (n < p.N) store1<TOut>(Y + (int64_t)(row0 + c) * ldy + n, a);
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while another reads its sums
     }
 }
 
@@ -479,23 +574,6 @@ template <bool NV> struct PairCfg {
     static_assert(16 * kStages + 40 <= 256, "barriers");
 };
 
-// shared-memory address of the same object in CTA `rank` of the cluster
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank)
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -729,30 +807,56 @@ static bool encode_tiles_map(CUtensorMap *map, const void *base, int64_t trows, 
 // pieces of `step` rows that T rows in E groups can make
 static int64_t max_pieces(int64_t T, int64_t E, int64_t step) { return E == 0 ? (T + step - 1) / step : T / step + (E < T ? E : T); }
 
-template <bool NV, typename TOut, bool GATE>
-static razer_status launch_stream(const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, TOut *Y, cudaStream_t st)
+// CTAs that share one unit: as many (a power of two, at most 8) as leave every
+// CTA two stages and fit on the device at once, two per SM
+static int stream_splits(int64_t units, int64_t steps)
+{
+    int S = 1;
+    while (S < 8 && 2 * S * units <= 2 * (int64_t)sm_count() && 2 * S * 2 <= steps) S *= 2;
+    return S;
+}
+
+template <bool NV, typename TOut, bool GATE, typename TIn>
+static razer_status launch_stream(const TIn *X, const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, TOut *Y, cudaStream_t st)
 {
     static bool attr_set[64] = {false};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        if (cudaFuncSetAttribute(mx_stream_kernel<NV, TOut, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStreamSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(mx_stream_kernel<NV, TOut, GATE, TIn>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStreamSmem) != cudaSuccess)
             return RAZER_ERR_CUDA;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
     CUtensorMap mw, ma, msw, msa;
     const int64_t E = p.E ? p.E : 1, arows = p.E ? tile_rows_grouped(p.T, p.E) : tile_rows(p.T);
-    if (!encode_codes_map(&mw, codes_w, p.N * E, p.K, 128) || !encode_codes_map(&ma, codes_a, p.T, p.K, kBoxRows) ||
-        !encode_tiles_map(&msw, p.tiles_w, E * p.trows_w, p.ct, 1, kStepTiles<NV>) ||
-        !encode_tiles_map(&msa, p.tiles_a, arows, p.ct, 1, kStepTiles<NV>))
+    if (!encode_codes_map(&mw, codes_w, p.N * E, p.K, 128) || !encode_tiles_map(&msw, p.tiles_w, E * p.trows_w, p.ct, 1, kStepTiles<NV>))
         return RAZER_ERR_CUDA;
+    if (std::is_void<TIn>::value) {
+        if (!encode_codes_map(&ma, codes_a, p.T, p.K, kBoxRows) || !encode_tiles_map(&msa, p.tiles_a, arows, p.ct, 1, kStepTiles<NV>))
+            return RAZER_ERR_CUDA;
+    } else {
+        ma = mw;  // not used
+        msa = msw;
+    }
     const int ntiles = (p.N + 127) / 128;
-    const int64_t grid = max_pieces(p.T, p.E, kStreamRows) * ntiles;
-    if (grid > INT32_MAX) return RAZER_ERR_SHAPE;
+    const int64_t units = max_pieces(p.T, p.E, kStreamRows) * ntiles;
+    const int S = stream_splits(units, (p.K + kStepK - 1) / kStepK);
+    if (units * S > INT32_MAX) return RAZER_ERR_SHAPE;
     const int inject = fault_injection_enabled() ? 1 : 0;
-    if (launch_pdl(mx_stream_kernel<NV, TOut, GATE>, (unsigned)grid, (unsigned)kStreamThreads, (size_t)kStreamSmem, st, mw, ma, msw, msa, p,
-                   ntiles, Y,
-                   inject) != cudaSuccess)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * S));
+    cfg.blockDim = dim3(kStreamThreads);
+    cfg.dynamicSmemBytes = kStreamSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)S;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = S > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, mx_stream_kernel<NV, TOut, GATE, TIn>, mw, ma, msw, msa, p, X, ntiles, S, Y, inject) != cudaSuccess)
         return RAZER_ERR_CUDA;
     return RAZER_OK;
 }
@@ -798,21 +902,33 @@ static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, 
     return RAZER_OK;
 }
 
+static int64_t rows_per_group(int64_t T, int64_t E) { return E > 0 ? (T + E - 1) / E : T; }
+
 template <bool NV, typename TOut, bool GATE>
 static razer_status launch_mx(const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, TOut *Y, cudaStream_t st)
 {
-    const int64_t rows = p.E > 0 ? (p.T + p.E - 1) / p.E : p.T;  // rows of a group, on average
-    if (rows > 64) return launch_pair<NV, TOut, GATE>(codes_a, codes_w, p, kPairRows, Y, st);
-    return launch_stream<NV, TOut, GATE>(codes_a, codes_w, p, Y, st);
+    if (rows_per_group(p.T, p.E) > 64) return launch_pair<NV, TOut, GATE>(codes_a, codes_w, p, kPairRows, Y, st);
+    return launch_stream<NV, TOut, GATE, void>(nullptr, codes_a, codes_w, p, Y, st);
 }
 
 template <typename TOut>
-static razer_status run_mx_t(bool nv, const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, TOut *Y, cudaStream_t st)
+static razer_status run_mx_t(bool nv, const void *X, razer_dtype x_dt, const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, TOut *Y,
+                             cudaStream_t st)
 {
     if (p.K == 0) {
         const int64_t cols = p.gate ? p.N / 2 : p.N;
         mx_zero_kernel<TOut><<<sm_count() * 4, 256, 0, st>>>(p.offsets, p.E, p.T, cols, Y);
         return last_launch_status();
+    }
+    if (X) {
+        if (x_dt == RAZER_F16) {
+            const __half *x = reinterpret_cast<const __half *>(X);
+            if (p.gate) return launch_stream<false, TOut, true, __half>(x, nullptr, codes_w, p, Y, st);
+            return launch_stream<false, TOut, false, __half>(x, nullptr, codes_w, p, Y, st);
+        }
+        const __nv_bfloat16 *x = reinterpret_cast<const __nv_bfloat16 *>(X);
+        if (p.gate) return launch_stream<false, TOut, true, __nv_bfloat16>(x, nullptr, codes_w, p, Y, st);
+        return launch_stream<false, TOut, false, __nv_bfloat16>(x, nullptr, codes_w, p, Y, st);
     }
     if (p.gate) return nv ? launch_mx<true, TOut, true>(codes_a, codes_w, p, Y, st) : launch_mx<false, TOut, true>(codes_a, codes_w, p, Y, st);
     return nv ? launch_mx<true, TOut, false>(codes_a, codes_w, p, Y, st) : launch_mx<false, TOut, false>(codes_a, codes_w, p, Y, st);
@@ -820,9 +936,14 @@ static razer_status run_mx_t(bool nv, const uint8_t *codes_a, const uint8_t *cod
 
 }  // namespace mx
 
+// whether an online call quantizes inside the product (few rows per group)
+bool gemm_mx_fuses(int64_t T, int64_t E) { return mx::rows_per_group(T, E) <= mx::kFuseRows; }
+
 // E = 0: dense (offsets ignored); otherwise W is [E, N, K] and ts_w holds E
-// scales.  The caller has checked every argument; T, N > 0.
-razer_status run_gemm_mx(const uint8_t *codes_a, const uint8_t *tiles_a, const float *ts_a, int64_t T, const int32_t *offsets, int E,
+// scales.  X: the activations, to be quantized to MXFP4 inside the product
+// (gemm_mx_fuses), or NULL: they are packed.  The caller has checked every
+// argument; T, N > 0.
+razer_status run_gemm_mx(const void *X, razer_dtype x_dt, const uint8_t *codes_a, const uint8_t *tiles_a, const float *ts_a, int64_t T, const int32_t *offsets, int E,
                          const uint8_t *codes_w, const uint8_t *tiles_w, const float *ts_w, razer_format fmt, int64_t N, int64_t K, int gate,
                          void *Y, razer_dtype out_dt, cudaStream_t st)
 {
@@ -840,9 +961,9 @@ razer_status run_gemm_mx(const uint8_t *codes_a, const uint8_t *tiles_a, const f
     p.ct = (int)mx::tile_cols(nv, K);
     p.trows_w = (int)mx::tile_rows(N);
     p.gate = gate;
-    if (out_dt == RAZER_F32) return mx::run_mx_t<float>(nv, codes_a, codes_w, p, reinterpret_cast<float *>(Y), st);
-    if (out_dt == RAZER_F16) return mx::run_mx_t<__half>(nv, codes_a, codes_w, p, reinterpret_cast<__half *>(Y), st);
-    return mx::run_mx_t<__nv_bfloat16>(nv, codes_a, codes_w, p, reinterpret_cast<__nv_bfloat16 *>(Y), st);
+    if (out_dt == RAZER_F32) return mx::run_mx_t<float>(nv, X, x_dt, codes_a, codes_w, p, reinterpret_cast<float *>(Y), st);
+    if (out_dt == RAZER_F16) return mx::run_mx_t<__half>(nv, X, x_dt, codes_a, codes_w, p, reinterpret_cast<__half *>(Y), st);
+    return mx::run_mx_t<__nv_bfloat16>(nv, X, x_dt, codes_a, codes_w, p, reinterpret_cast<__nv_bfloat16 *>(Y), st);
 }
 
 }  // namespace razer

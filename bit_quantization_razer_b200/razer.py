@@ -398,22 +398,27 @@ def razer_gemm(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, ts: t
 # Scale tiles are uint8 tensors [..., tile rows, tile columns, 512]; include/razer.h
 # gives their layout and that of row groups.
 
+def _mx_bad(fn: str, name: str, t, shape, dtype, dev):
+    got = "None" if t is None else f"{tuple(t.shape)} {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}"
+    raise ValueError(f"{fn}: {name} must be a contiguous {tuple(shape)} {dtype} tensor on {dev}, got {got}")
+
+
 def _mx_shape(fn: str, name: str, t, shape, dtype, dev):
     """t is a contiguous tensor of this shape, type and device (the library sees only its address)."""
-    if t is None or tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev or not t.is_contiguous():
-        got = "None" if t is None else f"{tuple(t.shape)} {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}"
-        raise ValueError(f"{fn}: {name} must be a contiguous {tuple(shape)} {dtype} tensor on {dev}, got {got}")
+    if t is None or t.shape != shape or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+        _mx_bad(fn, name, t, shape, dtype, dev)
     return t
 
 
-def _mx_call(fn: str, dev, stream, *args):
+def _mx_call(fn: str, call, dev, stream, *args):
     """Calls the library with dev current and, without a stream, on dev's current stream."""
-    call = getattr(load(), fn)
-    if dev.index == torch.cuda.current_device():
-        _check(fn, call(*args, _stream(stream)))
-    else:
+    if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            _check(fn, call(*args, _stream(stream)))
+            return _mx_call(fn, call, dev, stream, *args)
+    # the raw handle: torch.cuda.current_stream() costs 3 us, as much as a launch
+    st = call(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream)
+    if st != RAZER_OK:
+        raise RazerError(fn, st)
 
 
 def _mx_ptr(t):
@@ -437,10 +442,17 @@ def _mx_groups(fn: str, offsets, dev) -> int:
     return offsets.shape[0] - 1
 
 
+def _mx_tiles(R: int, K: int, block: int, groups: int = 0) -> tuple[int, int, int]:
+    return (R // 128 + groups if groups else -(-R // 128), -(-K // (4 * block)), 512)
+
+
+def _mx_block(fmt) -> int:
+    return 16 if _fmt(fmt) == RAZER_FMT_NVFP4 else 32
+
+
 def razer_scale_tiles_shape(R: int, K: int, fmt="mxfp4", groups: int = 0) -> tuple[int, int, int]:
     """Shape of the scale tiles of [R, K] codes, or of R rows in `groups` row groups."""
-    per = 4 * (16 if _fmt(fmt) == RAZER_FMT_NVFP4 else 32)
-    return (R // 128 + groups if groups else -(-R // 128), -(-K // per), 512)
+    return _mx_tiles(R, K, _mx_block(fmt), groups)
 
 
 def razer_quantize_mx(X: torch.Tensor, offsets: torch.Tensor | None = None, *, codes=None, scales=None, stream=None):
@@ -451,10 +463,11 @@ def razer_quantize_mx(X: torch.Tensor, offsets: torch.Tensor | None = None, *, c
     M, K = _mx_matrix(fn, "X", X)
     dev = X.device
     E = _mx_groups(fn, offsets, dev)
-    shape = razer_scale_tiles_shape(M, K, "mxfp4", E)
-    codes = torch.empty((M, K // 2), dtype=torch.uint8, device=dev) if codes is None else _mx_shape(fn, "codes", codes, (M, K // 2), torch.uint8, dev)
-    scales = torch.empty(shape, dtype=torch.uint8, device=dev) if scales is None else _mx_shape(fn, "scales", scales, shape, torch.uint8, dev)
-    _mx_call(fn, dev, stream, X.data_ptr(), _DT.get(X.dtype, -1), M, K, _mx_ptr(offsets), E, codes.data_ptr(), scales.data_ptr())
+    r, c, b = shape = _mx_tiles(M, K, 32, E)
+    codes = torch.empty(M, K // 2, dtype=torch.uint8, device=dev) if codes is None else _mx_shape(fn, "codes", codes, (M, K // 2), torch.uint8, dev)
+    scales = torch.empty(r, c, b, dtype=torch.uint8, device=dev) if scales is None else _mx_shape(fn, "scales", scales, shape, torch.uint8, dev)
+    _mx_call(fn, load().razer_quantize_mx, dev, stream, X.data_ptr(), _DT.get(X.dtype, -1), M, K, _mx_ptr(offsets), E, codes.data_ptr(),
+             scales.data_ptr())
     return codes, scales
 
 
@@ -462,13 +475,14 @@ def razer_dequant_mx(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torch.
                      out=None, stream=None):
     """Decode MXFP4 codes [M, K/2] with their scale tiles to [M, K] (one rounding to out_dtype)."""
     fn = "razer_dequant_mx"
-    M, K2 = _mx_matrix(fn, "codes", codes)
+    M, K2 = shape = _mx_matrix(fn, "codes", codes)
     dev, K = codes.device, 2 * K2
     E = _mx_groups(fn, offsets, dev)
-    _mx_shape(fn, "codes", codes, (M, K2), torch.uint8, dev)
-    _mx_shape(fn, "scales", scales, razer_scale_tiles_shape(M, K, "mxfp4", E), torch.uint8, dev)
-    out = torch.empty((M, K), dtype=out_dtype, device=dev) if out is None else _mx_shape(fn, "out", out, (M, K), out_dtype, dev)
-    _mx_call(fn, dev, stream, codes.data_ptr(), scales.data_ptr(), M, K, _mx_ptr(offsets), E, out.data_ptr(), _DT.get(out.dtype, -1))
+    _mx_shape(fn, "codes", codes, shape, torch.uint8, dev)
+    _mx_shape(fn, "scales", scales, _mx_tiles(M, K, 32, E), torch.uint8, dev)
+    out = torch.empty(M, K, dtype=out_dtype, device=dev) if out is None else _mx_shape(fn, "out", out, (M, K), out.dtype, dev)
+    _mx_call(fn, load().razer_dequant_mx, dev, stream, codes.data_ptr(), scales.data_ptr(), M, K, _mx_ptr(offsets), E, out.data_ptr(),
+             _DT.get(out.dtype, -1))
     return out
 
 
@@ -484,8 +498,9 @@ def razer_tile_scales(scales: torch.Tensor, offsets: torch.Tensor | None = None,
     E = _mx_groups(fn, offsets, dev)
     R, C = shape[-2:]
     tiles = (*shape[:-2], R // 128 + E if E else -(-R // 128), -(-C // 4), 512)
-    out = torch.empty(tiles, dtype=torch.uint8, device=dev) if out is None else _mx_shape(fn, "out", out, tiles, torch.uint8, dev)
-    _mx_call(fn, dev, stream, scales.data_ptr(), shape[0] if len(shape) == 3 else 1, R, C, _mx_ptr(offsets), E, out.data_ptr())
+    out = torch.empty(*tiles, dtype=torch.uint8, device=dev) if out is None else _mx_shape(fn, "out", out, tiles, torch.uint8, dev)
+    _mx_call(fn, load().razer_tile_scales, dev, stream, scales.data_ptr(), shape[0] if len(shape) == 3 else 1, R, C, _mx_ptr(offsets), E,
+             out.data_ptr())
     return out
 
 
@@ -495,39 +510,41 @@ def _mx_act(fn: str, act) -> int:
     return ACTS[act]
 
 
-def _mx_weights(fn: str, codes_w, scales_w, E: int, K: int, fmt, dev, ts_w=None) -> int:
+def _mx_weights(fn: str, codes_w, scales_w, E: int, K: int, block: int, dev, ts_w=None) -> int:
     """Checks packed weights [N, K/2], or [E, N, K/2] for row groups; returns N."""
-    lead = (E,) if E else ()
-    if codes_w.dim() != 2 + len(lead):
-        raise ValueError(f"{fn}: codes_w must be {'[E, N, K/2]' if E else '[N, K/2]'}, got {tuple(codes_w.shape)}")
-    N = codes_w.shape[-2]
-    _mx_shape(fn, "codes_w", codes_w, (*lead, N, K // 2), torch.uint8, dev)
-    _mx_shape(fn, "scales_w", scales_w, (*lead, *razer_scale_tiles_shape(N, K, fmt)), torch.uint8, dev)
+    shape = codes_w.shape
+    if len(shape) != (3 if E else 2):
+        raise ValueError(f"{fn}: codes_w must be {'[E, N, K/2]' if E else '[N, K/2]'}, got {tuple(shape)}")
+    N = shape[-2]
+    _mx_shape(fn, "codes_w", codes_w, (E, N, K // 2) if E else (N, K // 2), torch.uint8, dev)
+    tiles = _mx_tiles(N, K, block)
+    _mx_shape(fn, "scales_w", scales_w, (E, *tiles) if E else tiles, torch.uint8, dev)
     if ts_w is not None:
         _mx_shape(fn, "ts_w", ts_w, (E or 1,), torch.float32, dev)
     return N
 
 
-def _mx_out(fn: str, out, rows: int, N: int, act: int, out_dtype, dev, make=torch.empty):
-    shape = (rows, N // 2 if act else N)
-    if out is None:
-        return make(shape, dtype=out_dtype, device=dev)
-    return _mx_shape(fn, "out", out, shape, out.dtype, dev)
+def _mx_out(fn: str, out, rows: int, N: int, act: int, out_dtype, dev, groups: int):
+    cols = N // 2 if act else N
+    if out is None:  # rows of no group are not written
+        return (torch.zeros if groups else torch.empty)(rows, cols, dtype=out_dtype, device=dev)
+    return _mx_shape(fn, "out", out, (rows, cols), out.dtype, dev)
 
 
-def _mx_product(fn, codes_a, scales_a, offsets, codes_w, scales_w, fmt, out_dtype, ts_a, ts_w, act, out, stream):
-    T, K2 = _mx_matrix(fn, "codes_a", codes_a)
+def _mx_product(fn, call, codes_a, scales_a, offsets, codes_w, scales_w, fmt, out_dtype, ts_a, ts_w, act, out, stream):
+    T, K2 = shape = _mx_matrix(fn, "codes_a", codes_a)
     dev, K = codes_a.device, 2 * K2
     E, f, a = _mx_groups(fn, offsets, dev), _fmt(fmt), _mx_act(fn, act)
-    _mx_shape(fn, "codes_a", codes_a, (T, K2), torch.uint8, dev)
-    _mx_shape(fn, "scales_a", scales_a, razer_scale_tiles_shape(T, K, f, E), torch.uint8, dev)
+    block = _mx_block(f)
+    _mx_shape(fn, "codes_a", codes_a, shape, torch.uint8, dev)
+    _mx_shape(fn, "scales_a", scales_a, _mx_tiles(T, K, block, E), torch.uint8, dev)
     if ts_a is not None:
         _mx_shape(fn, "ts_a", ts_a, (1,), torch.float32, dev)
-    N = _mx_weights(fn, codes_w, scales_w, E, K, f, dev, ts_w)
-    out = _mx_out(fn, out, T, N, a, out_dtype, dev, torch.zeros if E else torch.empty)
-    rows = (codes_a.data_ptr(), scales_a.data_ptr(), _mx_ptr(ts_a), T)
-    _mx_call(fn, dev, stream, *rows, *((offsets.data_ptr(), E) if E else ()), codes_w.data_ptr(), scales_w.data_ptr(), _mx_ptr(ts_w), f, N, K,
-             a, out.data_ptr(), _DT.get(out.dtype, -1))
+    N = _mx_weights(fn, codes_w, scales_w, E, K, block, dev, ts_w)
+    out = _mx_out(fn, out, T, N, a, out_dtype, dev, E)
+    groups = (offsets.data_ptr(), E) if E else ()
+    _mx_call(fn, call, dev, stream, codes_a.data_ptr(), scales_a.data_ptr(), _mx_ptr(ts_a), T, *groups, codes_w.data_ptr(), scales_w.data_ptr(),
+             _mx_ptr(ts_w), f, N, K, a, out.data_ptr(), _DT.get(out.dtype, -1))
     return out
 
 
@@ -536,7 +553,8 @@ def razer_gemm_mx(codes_a: torch.Tensor, scales_a: torch.Tensor, codes_w: torch.
     """Y [M, N] = ts_a * ts_w * deq(A [M, K]) . deq(W [N, K])^T of packed operands
     (codes and scale tiles; fmt "mxfp4" or "nvfp4") on the block-scaled tensor
     cores.  act="silu_mul": W's rows alternate gate and up, Y [M, N/2]."""
-    return _mx_product("razer_gemm_mx", codes_a, scales_a, None, codes_w, scales_w, fmt, out_dtype, ts_a, ts_w, act, out, stream)
+    return _mx_product("razer_gemm_mx", load().razer_gemm_mx, codes_a, scales_a, None, codes_w, scales_w, fmt, out_dtype, ts_a, ts_w, act, out,
+                       stream)
 
 
 def razer_gemm_mx_grouped(codes_a: torch.Tensor, scales_a: torch.Tensor, offsets: torch.Tensor, codes_w: torch.Tensor,
@@ -547,24 +565,28 @@ def razer_gemm_mx_grouped(codes_a: torch.Tensor, scales_a: torch.Tensor, offsets
     no group are not written (zeros, where the output is made here)."""
     if offsets is None:
         raise ValueError("razer_gemm_mx_grouped: offsets are needed")
-    return _mx_product("razer_gemm_mx_grouped", codes_a, scales_a, offsets, codes_w, scales_w, fmt, out_dtype, ts_a, ts_w, act, out, stream)
+    return _mx_product("razer_gemm_mx_grouped", load().razer_gemm_mx_grouped, codes_a, scales_a, offsets, codes_w, scales_w, fmt, out_dtype, ts_a,
+                       ts_w, act, out, stream)
 
 
-def _mx_online(fn, X, offsets, codes_w, scales_w, out_dtype, act, out, workspace, stream):
+def _mx_online(fn, call, X, offsets, codes_w, scales_w, out_dtype, act, out, workspace, stream):
     T, K = _mx_matrix(fn, "X", X)
     dev = X.device
     E, a = _mx_groups(fn, offsets, dev), _mx_act(fn, act)
-    N = _mx_weights(fn, codes_w, scales_w, E, K, RAZER_FMT_MXFP4, dev)
-    out = _mx_out(fn, out, T, N, a, out_dtype, dev, torch.zeros if E else torch.empty)
-    L = load()
-    need = L.razer_gemm_mx_grouped_workspace_size(T, K, E) if E else L.razer_workspace_size(RAZER_OP_GEMM_MX_ONLINE, T, N, K)
+    N = _mx_weights(fn, codes_w, scales_w, E, K, 32, dev)
+    out = _mx_out(fn, out, T, N, a, out_dtype, dev, E)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        need = load().razer_gemm_mx_grouped_workspace_size(T, K, E)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = need
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"{fn}: workspace must be a contiguous tensor on {dev}")
-    _mx_call(fn, dev, stream, X.data_ptr(), _DT.get(X.dtype, -1), T, *((offsets.data_ptr(), E) if E else ()), codes_w.data_ptr(),
-             scales_w.data_ptr(), N, K, a, out.data_ptr(), _DT.get(out.dtype, -1), workspace.data_ptr(),
-             workspace.numel() * workspace.element_size())
+    else:
+        ws = workspace.numel() * workspace.element_size()
+    groups = (offsets.data_ptr(), E) if E else ()
+    _mx_call(fn, call, dev, stream, X.data_ptr(), _DT.get(X.dtype, -1), T, *groups, codes_w.data_ptr(), scales_w.data_ptr(), N, K, a,
+             out.data_ptr(), _DT.get(out.dtype, -1), _mx_ptr(workspace), ws)
     return out
 
 
@@ -572,7 +594,7 @@ def razer_gemm_mx_online(X: torch.Tensor, codes_w: torch.Tensor, scales_w: torch
                          workspace=None, stream=None):
     """Quantize X [M, K] (fp16/bf16) to MXFP4 and multiply it with MXFP4 weights
     in one call; equals razer_quantize_mx followed by razer_gemm_mx."""
-    return _mx_online("razer_gemm_mx_online", X, None, codes_w, scales_w, out_dtype, act, out, workspace, stream)
+    return _mx_online("razer_gemm_mx_online", load().razer_gemm_mx_online, X, None, codes_w, scales_w, out_dtype, act, out, workspace, stream)
 
 
 def razer_gemm_mx_grouped_online(X: torch.Tensor, offsets: torch.Tensor, codes_w: torch.Tensor, scales_w: torch.Tensor,
@@ -580,7 +602,8 @@ def razer_gemm_mx_grouped_online(X: torch.Tensor, offsets: torch.Tensor, codes_w
     """razer_quantize_mx and razer_gemm_mx_grouped in one call, X [T, K] (fp16/bf16)."""
     if offsets is None:
         raise ValueError("razer_gemm_mx_grouped_online: offsets are needed")
-    return _mx_online("razer_gemm_mx_grouped_online", X, offsets, codes_w, scales_w, out_dtype, act, out, workspace, stream)
+    return _mx_online("razer_gemm_mx_grouped_online", load().razer_gemm_mx_grouped_online, X, offsets, codes_w, scales_w, out_dtype, act, out,
+                      workspace, stream)
 
 
 def razer_gemm_mx_grouped_workspace_size(T: int, K: int, groups: int) -> int:

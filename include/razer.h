@@ -554,7 +554,9 @@ razer_status razer_gemm_mx_grouped(const uint8_t *codes_a, const uint8_t *scales
  * call; Y equals that of the two calls.
  *   workspace  razer_workspace_size(RAZER_OP_GEMM_MX_ONLINE, M, N, K) or
  *              razer_gemm_mx_grouped_workspace_size(T, K, E) bytes (16-byte
- *              aligned; contents on entry ignored): the packed activations
+ *              aligned; contents on entry ignored): the packed activations.  0
+ *              bytes (NULL) for up to 16 rows, or 16 per group on average: the
+ *              product's kernel then quantizes them itself, in one launch.
  */
 razer_status razer_gemm_mx_online(const void *X, razer_dtype x_dt, int64_t M, const uint8_t *codes_w,
                                   const uint8_t *scales_w, int64_t N, int64_t K, razer_act act, void *Y,

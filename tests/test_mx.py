@@ -68,8 +68,11 @@ def test_sizes(lib):
     assert R.razer_scale_tiles_shape(300, 160, "nvfp4") == (3, 3, 512)
     assert R.razer_scale_tiles_shape(300, 160, "mxfp4", 7) == (9, 2, 512)
     assert R.razer_workspace_size(R.RAZER_OP_GEMM_MX_ONLINE, 300, 64, 160) == 24064 + 3 * 2 * 512
-    assert R.razer_gemm_mx_grouped_workspace_size(300, 160, 7) == 24064 + 9 * 2 * 512
+    assert R.razer_gemm_mx_grouped_workspace_size(300, 160, 7) == 24064 + 9 * 2 * 512  # 43 rows a group
     assert R.razer_gemm_mx_grouped_workspace_size(0, 160, 7) == 0
+    # few rows are quantized inside the product
+    assert R.razer_workspace_size(R.RAZER_OP_GEMM_MX_ONLINE, 16, 64, 160) == 0 < R.razer_workspace_size(R.RAZER_OP_GEMM_MX_ONLINE, 17, 64, 160)
+    assert R.razer_gemm_mx_grouped_workspace_size(7 * 16, 160, 7) == 0 < R.razer_gemm_mx_grouped_workspace_size(7 * 16 + 1, 160, 7)
 
 
 def test_quantizer_refusals(lib):
@@ -123,18 +126,18 @@ def test_product_refusals(lib):
 
 def test_online_refusals(lib):
     g = lib.razer_gemm_mx_online
-    def a(x=FAKE, xdt=1, M=4, cw=FAKE, sw=FAKE, N=8, K=64, act=0, y=FAKE, dt=1, ws=FAKE, wsb=1 << 20):
+    def a(x=FAKE, xdt=1, M=40, cw=FAKE, sw=FAKE, N=8, K=64, act=0, y=FAKE, dt=1, ws=FAKE, wsb=1 << 20):
         return g(x, xdt, M, cw, sw, N, K, act, y, dt, ws, wsb, None)
-    need = R.razer_workspace_size(R.RAZER_OP_GEMM_MX_ONLINE, 4, 8, 64)
+    need = R.razer_workspace_size(R.RAZER_OP_GEMM_MX_ONLINE, 40, 8, 64)
     assert a(xdt=2) == 4 and a(xdt=8) == 1 and a(K=48) == 2 and a(x=None) == 1 and a(x=ODD) == 3
     assert a(ws=None) == 5 and a(wsb=need - 1) == 5 and a(ws=ODD) == 3
     assert a(act=1, N=9) == 2 and a(act=7) == 1 and a(cw=None) == 1 and a(sw=ODD) == 3
     assert a(M=0, x=None, ws=None, wsb=0) == 0
     h = lib.razer_gemm_mx_grouped_online
-    def b(off=FAKE, E=2, T=4, ws=FAKE, wsb=1 << 20):
+    def b(off=FAKE, E=2, T=40, ws=FAKE, wsb=1 << 20):
         return h(FAKE, 1, T, off, E, FAKE, FAKE, 8, 64, 0, FAKE, 1, ws, wsb, None)
     assert b(E=0) == 2 and b(off=None) == 1 and b(off=BYTE) == 3 and b(ws=None) == 5
-    assert b(wsb=R.razer_gemm_mx_grouped_workspace_size(4, 64, 2) - 1) == 5
+    assert b(wsb=R.razer_gemm_mx_grouped_workspace_size(40, 64, 2) - 1) == 5
 
 
 def test_older_calls_refuse_mxfp4(lib):
