@@ -479,9 +479,11 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
                 // 8 blocks a row: a block's 16 bytes of codes are one unit of the swizzle
                 for (int i = lane; i < count * 8; i += 32) {
                     const int r = i >> 3, c = i & 7;
-                    uint4 codes = make_uint4(0u, 0u, 0u, 0u);
-                    unsigned byte = 0u;
-                    if (k0 + 32 * c < p.K) byte = quantize_block<TIn>(X + (int64_t)(row0 + r) * p.K + k0 + 32 * c, codes);
+                    uint4 v[4], codes;
+                    const uint4 *x = reinterpret_cast<const uint4 *>(X + (int64_t)(row0 + r) * p.K + k0 + 32 * c);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) v[j] = k0 + 32 * c < p.K ? __ldg(x + j) : make_uint4(0u, 0u, 0u, 0u);
+                    const unsigned byte = encode_block<TIn>(v, codes);
                     *reinterpret_cast<uint4 *>(b0 + r * 128 + ((c ^ (r & 7)) << 4)) = codes;
                     sb[(c >> 2) * kTileBytes + (r & 31) * 16 + (r >> 5) * 4 + (c & 3)] = (uint8_t)byte;
                 }
