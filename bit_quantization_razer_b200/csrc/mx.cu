@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(256, kQuantizeCtas) quantize_mx_kernel(const T
     const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
     const int64_t kb = K / 32, ct = tile_cols(false, K), nb = M * kb;
-    if (E > 0 && blockIdx.x == 0) check_offsets(offsets, E, (int)M);
+    if (E > 0 && blockIdx.x == 0 && threadIdx.x < 32) check_offsets(offsets, E, (int)M);
     auto fetch = [&](int64_t task, int slot) {
         const uint4 *src = reinterpret_cast<const uint4 *>(x) + task * 128;
 #pragma unroll
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(256) dequant_mx_kernel(const uint8_t *__restri
     const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
     const int64_t ct = tile_cols(false, K), total = M * chunks;
-    if (E > 0 && blockIdx.x == 0) check_offsets(offsets, E, (int)M);
+    if (E > 0 && blockIdx.x == 0 && threadIdx.x < 32) check_offsets(offsets, E, (int)M);
     for (int64_t task = warp; task < total; task += warps) {
         const int64_t row = div_small(task, chunks);
         const int col = (int)(task - row * chunks) * kTaskCols;
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(128) tile_scales_kernel(const uint8_t *__restr
     const int64_t cc = blockIdx.x % col_chunks, tr = blockIdx.x / col_chunks;  // tr counts the tile rows of every batch
     const int i = threadIdx.x;
     int64_t row, end;
-    if (E > 0 && blockIdx.x == 0) check_offsets(offsets, E, (int)R);
+    if (E > 0 && blockIdx.x == 0 && threadIdx.x < 32) check_offsets(offsets, E, (int)R);
     if (E > 0) {
         // the last group whose first tile row is at most tr
         int lo = 0, hi = E;

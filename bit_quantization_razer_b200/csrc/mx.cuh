@@ -37,10 +37,10 @@ __device__ __forceinline__ int group_edge(const int32_t *offsets, int i, int T)
     const int v = __ldg(offsets + i);
     return v < 0 ? 0 : (v > T ? T : v);
 }
-// reports offsets that break the rules in the device status word (one CTA of a launch calls it)
+// reports offsets that break the rules in the device status word (one warp of a launch calls it)
 __device__ __forceinline__ void check_offsets(const int32_t *offsets, int E, int T)
 {
-    for (int i = threadIdx.x; i <= E; i += blockDim.x) {
+    for (int i = threadIdx.x & 31; i <= E; i += 32) {
         const int v = __ldg(offsets + i);
         if (v < 0 || v > T || (i > 0 && v < __ldg(offsets + i - 1))) set_device_status(RAZER_ERR_INVALID_ARG);
     }

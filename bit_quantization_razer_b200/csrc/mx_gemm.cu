@@ -329,7 +329,7 @@ template <bool NV> struct StreamCfg {
     static constexpr uint32_t kScaleCols = kStepTiles<NV> * 4;
     static constexpr uint32_t kCols = 256;
     static_assert(kStreamRows + 2 * kScaleCols <= kCols, "two CTAs share an SM's tensor memory");
-    static_assert(kStreamRing / (kA + kBox + 2 * kS) <= kStreamMaxStages && kStreamMaxStages <= kStreamWorkers, "barriers and a warp for every stage");
+    static_assert(kStreamRing / (kA + kBox + 2 * kS) <= kStreamMaxStages, "barriers for every stage");
     static_assert(kStreamRing / (kA + kStreamRows * 128 + 2 * kS) >= 3, "a ring for the widest unit");
 };
 static_assert(kStreamRows * 128 * 4 <= kStreamRing, "the sums of a cluster's CTA");
@@ -353,54 +353,48 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int z = splits > 1 ? (int)cluster_rank() : 0, block = blockIdx.x / (unsigned)splits;
     const int n0 = block % ntiles * 128, t = block / ntiles;
+    const int steps = (p.K + kStepK - 1) / kStepK;
+    // this CTA's stages: g0 .. g0 + nk - 1
+    const int g0 = (int)((int64_t)steps * z / splits), g1 = (int)((int64_t)steps * (z + 1) / splits);
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStreamMaxStages; s++) {
-            mbar_init(full + 8 * s, kFused ? 2 : 1);  // the producer, and the warp that quantizes the stage
-            mbar_init(empty + 8 * s, 1);
-        }
-        mbar_init(acc_full, 1);
-        mbar_init(drained, 1);
-        *abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
+    pdl_trigger();
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr((const void *)tmem_slot)),
                      "n"(Cfg::kCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        tc_fence_before();
     }
-    pdl_wait();  // the operands may come from an earlier kernel of the stream
-    if (p.E > 0 && blockIdx.x == 0) check_offsets(p.offsets, p.E, p.T);
     if (warp == 0) {
+        // ---------------- producer ----------------
+        // It sets up the barriers itself and fills the ring before it meets the
+        // other warps: the first copies are on their way while they start.
+        const uint32_t lead = elect_one();
+        if (lead) {
+            for (int s = 0; s < kStreamMaxStages; s++) {
+                mbar_init(full + 8 * s, kFused ? 5 : 1);  // the producer, and the four warps that quantize the stage
+                mbar_init(empty + 8 * s, 1);
+            }
+            mbar_init(acc_full, 1);
+            mbar_init(drained, 1);
+            *abort_flag = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncwarp();
+        pdl_wait();  // the operands may come from an earlier kernel of the stream
         const RowUnit u = row_unit(p, t, kStreamRows);
-        if (lane == 0) {
+        if (lead) {
             unit_slot[0] = u.e;
             unit_slot[1] = u.row0;
             unit_slot[2] = u.count;
-            unit_slot[3] = u.trow;
         }
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    const int ue = unit_slot[0], row0 = unit_slot[1], count = unit_slot[2], trow = unit_slot[3];
-    // this CTA's stages g0 .. g0 + nk - 1
-    const int steps = (p.K + kStepK - 1) / kStepK;
-    const int g0 = (int)((int64_t)steps * z / splits), nk = count > 0 ? (int)((int64_t)steps * (z + 1) / splits) - g0 : 0;
-    const int boxes = (count + kBoxRows - 1) / kBoxRows;
-    const uint32_t bbytes = (uint32_t)boxes * Cfg::kBox, stage = Cfg::kA + bbytes + 2 * Cfg::kS;
-    const uint32_t stages = kStreamRing / stage;
-
-    if (warp == 0) {
-        // ---------------- producer ----------------
-        const uint32_t lead = elect_one();
-        const int wrow = ue * p.N + n0, srow = ue * p.trows_w + n0 / kTileRows;
-        int g = 0;
+        const int nk = u.count > 0 ? g1 - g0 : 0, boxes = (u.count + kBoxRows - 1) / kBoxRows;
+        const uint32_t bbytes = (uint32_t)boxes * Cfg::kBox, stage = Cfg::kA + bbytes + 2 * Cfg::kS, stages = kStreamRing / stage;
+        const int wrow = u.e * p.N + n0, srow = u.e * p.trows_w + n0 / kTileRows;
         uint32_t s = 0, ph = 0;  // the ring: stage, how often it went round
         bool ok = true;
-        for (; g < nk; g++) {
-            if (!mbar_wait_all(empty + 8 * s, ph ^ 1u, abort_flag)) {
+        if (nk <= 0) __syncthreads();
+        for (int g = 0; g < nk; g++) {
+            if (g >= (int)stages && !mbar_wait_all(empty + 8 * s, ph ^ 1u, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -413,14 +407,15 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
                 tma_load_2d(a0, &tmap_w, c0, wrow, f);
                 tma_load_3d(s0, &tmap_sw, 0, t0, srow, f);
                 if constexpr (!kFused) {
-                    for (int b = 0; b < boxes; b++) tma_load_2d(a0 + Cfg::kA + b * Cfg::kBox, &tmap_a, c0, row0 + b * kBoxRows, f);
-                    tma_load_3d(s0 + Cfg::kS, &tmap_sa, 0, t0, trow, f);
+                    for (int b = 0; b < boxes; b++) tma_load_2d(a0 + Cfg::kA + b * Cfg::kBox, &tmap_a, c0, u.row0 + b * kBoxRows, f);
+                    tma_load_3d(s0 + Cfg::kS, &tmap_sa, 0, t0, u.trow, f);
                 }
             }
             if (++s == stages) {
                 s = 0;
                 ph ^= 1u;
             }
+            if (g + 1 == min(nk, (int)stages)) __syncthreads();  // the ring is full, or all is on its way
         }
         if (!ok) {
             // loads already issued land within microseconds; their barriers may
@@ -430,6 +425,19 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             }
             __syncwarp();
         }
+    } else {
+        pdl_wait();
+        if (p.E > 0 && blockIdx.x == 0 && warp == 2) check_offsets(p.offsets, p.E, p.T);
+        __syncthreads();
+    }
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int ue = unit_slot[0], row0 = unit_slot[1], count = unit_slot[2], nk = count > 0 ? g1 - g0 : 0;
+    const uint32_t bbytes = (uint32_t)((count + kBoxRows - 1) / kBoxRows) * Cfg::kBox, stage = Cfg::kA + bbytes + 2 * Cfg::kS;
+    const uint32_t stages = kStreamRing / stage;
+
+    if (warp == 0) {
+        // done above
     } else if (warp == 1) {
         if (nk > 0) {
             // ---------------- MMA issuer ----------------
@@ -464,32 +472,46 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     } else {
         bool ok = true;
         if constexpr (kFused) {
-            // ---------------- quantizer: a warp for each place of the ring ----------------
-            // (a warp that went on to another place could be two rounds ahead of it,
-            // which a barrier's parity cannot tell from none)
-            const uint32_t s = (uint32_t)warp - 2;
-            uint32_t ph = 0;
-            for (int g = (int)s; g < nk && s < stages; g += (int)stages, ph ^= 1u) {
+            // ---------------- quantizer ----------------
+            // Warps 2-5 take the even stages, 6-9 the odd ones, a thread one block
+            // of 32 at a time (16 rows are one block each); the block of the next
+            // stage is on its way while this one is encoded.  (Two stages in turn:
+            // a warp that took every fourth could be two rounds of the ring ahead,
+            // which a barrier's parity cannot tell from none.)
+            const int group = (warp - 2) >> 2, tid = (threadIdx.x - 64) & 127;
+            uint4 v[4];
+            auto load = [&](int g, int i) {
+                const int r = i >> 3, k = (g0 + g) * kStepK + 32 * (i & 7);
+                const bool in = g < nk && i < count * 8 && k < p.K;  // past K: zeros
+                const uint4 *x = reinterpret_cast<const uint4 *>(X + (int64_t)(row0 + r) * p.K + k);
+#pragma unroll
+                for (int j = 0; j < 4; j++) v[j] = in ? __ldg(x + j) : make_uint4(0u, 0u, 0u, 0u);
+            };
+            load(group, tid);
+            uint32_t s = (uint32_t)group, ph = 0;
+            for (int g = group; g < nk; g += 2) {
                 if (!mbar_wait_all(empty + 8 * s, ph ^ 1u, abort_flag)) {
                     ok = false;
                     break;
                 }
                 uint8_t *b0 = smem + s * stage + Cfg::kA, *sb = b0 + bbytes + Cfg::kS;
-                const int k0 = (g0 + g) * kStepK;
                 // 8 blocks a row: a block's 16 bytes of codes are one unit of the swizzle
-                for (int i = lane; i < count * 8; i += 32) {
+                for (int i = tid; i < count * 8; i += 128) {
                     const int r = i >> 3, c = i & 7;
-                    uint4 v[4], codes;
-                    const uint4 *x = reinterpret_cast<const uint4 *>(X + (int64_t)(row0 + r) * p.K + k0 + 32 * c);
-#pragma unroll
-                    for (int j = 0; j < 4; j++) v[j] = k0 + 32 * c < p.K ? __ldg(x + j) : make_uint4(0u, 0u, 0u, 0u);
+                    uint4 codes;
                     const unsigned byte = encode_block<TIn>(v, codes);
+                    load(i + 128 < count * 8 ? g : g + 2, i + 128 < count * 8 ? i + 128 : tid);
                     *reinterpret_cast<uint4 *>(b0 + r * 128 + ((c ^ (r & 7)) << 4)) = codes;
                     sb[(c >> 2) * kTileBytes + (r & 31) * 16 + (r >> 5) * 4 + (c & 3)] = (uint8_t)byte;
                 }
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full + 8 * s);
+                s += 2;
+                if (s >= stages) {
+                    s -= stages;
+                    ph ^= 1u;
+                }
             }
         }
         // ---------------- epilogue ----------------
@@ -614,6 +636,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    pdl_trigger();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; s++) {
@@ -638,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_wait();  // the activations come from an earlier kernel of the stream
-    if (p.E > 0 && blockIdx.x == 0) check_offsets(p.offsets, p.E, p.T);
+    if (p.E > 0 && blockIdx.x == 0 && warp == 2) check_offsets(p.offsets, p.E, p.T);
     const int nk = (p.K + kStepK - 1) / kStepK;
 
     if (warp == 0 || warp == kPairEpiWarps + 2) {
@@ -809,13 +832,18 @@ static bool encode_tiles_map(CUtensorMap *map, const void *base, int64_t trows, 
 // pieces of `step` rows that T rows in E groups can make
 static int64_t max_pieces(int64_t T, int64_t E, int64_t step) { return E == 0 ? (T + step - 1) / step : T / step + (E < T ? E : T); }
 
-// CTAs that share one unit: as many (a power of two, at most 8) as leave every
-// CTA two stages and fit on the device at once, two per SM
+// CTAs that share one unit along K: the power of two up to 8 that leaves the
+// busiest SM least to do (units * S CTAs, dealt out over the SMs, 1 / S of a
+// unit each; two stages at least; all of them resident), the smaller on a tie, since joining the sums
+// costs about 0.5 us.  MXFP4, packed, one row: 32 units of K = 4096 in 7.3 /
+// 6.3 / 5.8 / 6.5 us for S = 1 / 2 / 4 / 8; 112 units 9.2 / 9.2 / 13 / 21.
 static int stream_splits(int64_t units, int64_t steps)
 {
-    int S = 1;
-    while (S < 8 && 2 * S * units <= 2 * (int64_t)sm_count() && 2 * S * 2 <= steps) S *= 2;
-    return S;
+    const int64_t sms = sm_count();
+    int best = 1;
+    for (int S = 2; S <= 8 && 2 * S <= steps && units * S <= 2 * sms; S *= 2)
+        if ((units * S + sms - 1) / sms * best < (units * best + sms - 1) / sms * S) best = S;
+    return best;
 }
 
 template <bool NV, typename TOut, bool GATE, typename TIn>
