@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(256, kQuantizeCtas) quantize_mx_kernel(const T
 {
     __shared__ uint4 ring[8][kRing][128];
     pdl_trigger();
+    pdl_wait();
     const int lane = threadIdx.x & 31;
     uint4(*mine)[128] = ring[threadIdx.x >> 5];
     const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__(256) dequant_mx_kernel(const uint8_t *__restri
                                                          TOut *__restrict__ out)
 {
     pdl_trigger();
+    pdl_wait();
     constexpr int kPer = 16 / (int)sizeof(TOut), kIters = kTaskCols / (32 * kPer);
     const int lane = threadIdx.x & 31;
     const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -246,6 +248,8 @@ __global__ void __launch_bounds__(128) tile_scales_kernel(const uint8_t *__restr
                                                           uint8_t *__restrict__ tiles)
 {
     __shared__ __align__(16) uint8_t buf[4 * kTileBytes];
+    pdl_trigger();
+    pdl_wait();
     const int64_t cc = blockIdx.x % col_chunks, tr = blockIdx.x / col_chunks;  // tr counts the tile rows of every batch
     const int i = threadIdx.x;
     int64_t row, end;
@@ -306,11 +310,12 @@ razer_status run_quantize_mx(const void *X, razer_dtype dt, int64_t M, int64_t K
 {
     using namespace mx;
     const unsigned g = mx_grid((M * (K / 32) + 31) / 32, kQuantizeCtas);
+    cudaError_t e;
     if (dt == RAZER_F16)
-        quantize_mx_kernel<__half><<<g, 256, 0, st>>>(reinterpret_cast<const __half *>(X), M, K, offsets, E, codes, tiles);
+        e = launch_pdl(quantize_mx_kernel<__half>, g, 256u, 0, st, reinterpret_cast<const __half *>(X), M, K, offsets, E, codes, tiles);
     else
-        quantize_mx_kernel<__nv_bfloat16><<<g, 256, 0, st>>>(reinterpret_cast<const __nv_bfloat16 *>(X), M, K, offsets, E, codes, tiles);
-    return last_launch_status();
+        e = launch_pdl(quantize_mx_kernel<__nv_bfloat16>, g, 256u, 0, st, reinterpret_cast<const __nv_bfloat16 *>(X), M, K, offsets, E, codes, tiles);
+    return e == cudaSuccess ? RAZER_OK : RAZER_ERR_CUDA;
 }
 
 razer_status run_dequant_mx(const uint8_t *codes, const uint8_t *tiles, int64_t M, int64_t K, const int32_t *offsets, int E, void *out,
@@ -319,13 +324,14 @@ razer_status run_dequant_mx(const uint8_t *codes, const uint8_t *tiles, int64_t 
     using namespace mx;
     const int64_t chunks = (K + kTaskCols - 1) / kTaskCols;
     const unsigned g = mx_grid(M * chunks, 16);
+    cudaError_t e;
     if (dt == RAZER_F32)
-        dequant_mx_kernel<float><<<g, 256, 0, st>>>(codes, tiles, M, K, chunks, offsets, E, reinterpret_cast<float *>(out));
+        e = launch_pdl(dequant_mx_kernel<float>, g, 256u, 0, st, codes, tiles, M, K, chunks, offsets, E, reinterpret_cast<float *>(out));
     else if (dt == RAZER_F16)
-        dequant_mx_kernel<__half><<<g, 256, 0, st>>>(codes, tiles, M, K, chunks, offsets, E, reinterpret_cast<__half *>(out));
+        e = launch_pdl(dequant_mx_kernel<__half>, g, 256u, 0, st, codes, tiles, M, K, chunks, offsets, E, reinterpret_cast<__half *>(out));
     else
-        dequant_mx_kernel<__nv_bfloat16><<<g, 256, 0, st>>>(codes, tiles, M, K, chunks, offsets, E, reinterpret_cast<__nv_bfloat16 *>(out));
-    return last_launch_status();
+        e = launch_pdl(dequant_mx_kernel<__nv_bfloat16>, g, 256u, 0, st, codes, tiles, M, K, chunks, offsets, E, reinterpret_cast<__nv_bfloat16 *>(out));
+    return e == cudaSuccess ? RAZER_OK : RAZER_ERR_CUDA;
 }
 
 razer_status run_tile_scales(const uint8_t *rows, int64_t batch, int64_t R, int64_t C, const int32_t *offsets, int E, uint8_t *tiles,
@@ -335,8 +341,8 @@ razer_status run_tile_scales(const uint8_t *rows, int64_t batch, int64_t R, int6
     const int64_t ct = (C + 3) / 4, col_chunks = (ct + 3) / 4;
     const int64_t trows = E > 0 ? tile_rows_grouped(R, E) : tile_rows(R);
     const int vec = (C % 16 == 0 && (reinterpret_cast<uintptr_t>(rows) & 15) == 0) ? 1 : 0;
-    tile_scales_kernel<<<(unsigned)(batch * trows * col_chunks), 128, 0, st>>>(rows, R, C, ct, col_chunks, trows, offsets, E, vec, tiles);
-    return last_launch_status();
+    const cudaError_t e = launch_pdl(tile_scales_kernel, (unsigned)(batch * trows * col_chunks), 128u, 0, st, rows, R, C, ct, col_chunks, trows, offsets, E, vec, tiles);
+    return e == cudaSuccess ? RAZER_OK : RAZER_ERR_CUDA;
 }
 
 }  // namespace razer

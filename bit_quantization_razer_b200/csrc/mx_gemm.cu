@@ -151,7 +151,16 @@ __device__ __forceinline__ void issue_mmas(uint32_t lead, uint32_t acc, uint32_t
     }
 }
 
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// silu(g) * u = g / (1 + exp(-g)) * u.  16-bit outputs take the hardware's
+// 2^x and reciprocal: the exponent's rounding, |g| log2(e) 2^-24, bounds the
+// relative error by 6e-6 where the result is not yet 0 (|g| < 88), against the
+// 2^-9 (2^-12) of the output's own rounding; with expf and an IEEE division
+// the epilogue of 512 x 28672 x 4096 took longer than its MMAs.
+template <typename TOut> __device__ __forceinline__ float silu_mul(float g, float u)
+{
+    if constexpr (sizeof(TOut) == 2) return __fdividef(g, 1.0f + __expf(-g)) * u;
+    else return g / (1.0f + expf(-g)) * u;
+}
 
 // One product: N, K of the weights, T activation rows (in all groups), E = 0:
 // dense.  tiles_w holds trows_w tile rows per expert, ct tiles each.
@@ -176,54 +185,62 @@ struct RowUnit {
     int e, row0, count, trow, off;
 };
 
-// The t-th piece of up to `step` rows (a multiple of 64), counted over the
-// groups; a warp works it out together, 32 groups at a time.  count <= 0:
-// there is no such piece.
-__device__ __forceinline__ RowUnit row_unit(const Problem &p, int t, int step)
-{
-    RowUnit u = {0, 0, 0, 0, 0};
-    if (p.E == 0) {
-        u.row0 = t * step;
-        u.count = min(step, p.T - u.row0);
-        u.trow = u.row0 / kTileRows;
-        u.off = u.row0 % kTileRows;
-        return u;
-    }
-    const int lane = threadIdx.x & 31;
-    int before = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-        const int e = e0 + lane;
-        int start = 0, n = 0;
+// Finds the t-th piece of up to `step` rows (a multiple of 64), counted over
+// the groups, for a t that never falls: a warp keeps 32 groups at a time, a
+// lane one of them, and loads the next 32 when t has passed these.  (Reading
+// the offsets again for every unit cost each role some 0.4 us a unit.)
+struct RowWalk {
+    int e0, before, start, n, upto, total;  // first group; pieces before it; this lane's group; its pieces' inclusive sum; all 32's
+
+    __device__ __forceinline__ void load(const Problem &p, int step)
+    {
+        const int lane = threadIdx.x & 31, e = e0 + lane;
+        start = n = 0;
         if (e < p.E) {
             start = group_edge(p.offsets, e, p.T);
-            n = group_edge(p.offsets, e + 1, p.T) - start;
-            if (n < 0) n = 0;
+            n = max(group_edge(p.offsets, e + 1, p.T) - start, 0);
         }
-        const int pieces = (n + step - 1) / step;
-        int upto = pieces;
+        upto = (n + step - 1) / step;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, upto, d);
             if (lane >= d) upto += o;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + upto > t);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            const int first = before + __shfl_sync(0xffffffffu, upto - pieces, src);
-            start = __shfl_sync(0xffffffffu, start, src);
-            n = __shfl_sync(0xffffffffu, n, src);
-            const int in = (t - first) * step;
-            u.e = e0 + src;
-            u.row0 = start + in;
-            u.count = min(step, n - in);
-            u.trow = group_tile_row(start, u.e) + in / kTileRows;
-            u.off = in % kTileRows;
+        total = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    __device__ __forceinline__ void begin(const Problem &p, int step)
+    {
+        e0 = before = 0;
+        if (p.E > 0) load(p, step);
+    }
+    // count <= 0: there is no such piece
+    __device__ __forceinline__ RowUnit at(const Problem &p, int t, int step)
+    {
+        RowUnit u = {0, 0, 0, 0, 0};
+        if (p.E == 0) {
+            u.row0 = t * step;
+            u.count = min(step, p.T - u.row0);
+            u.trow = u.row0 / kTileRows;
+            u.off = u.row0 % kTileRows;
             return u;
         }
-        before += __shfl_sync(0xffffffffu, upto, 31);
+        while (t >= before + total) {
+            if (e0 + 32 >= p.E) return u;
+            before += total;
+            e0 += 32;
+            load(p, step);
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, before + upto > t)) - 1;
+        const int s0 = __shfl_sync(0xffffffffu, start, src), sn = __shfl_sync(0xffffffffu, n, src);
+        const int last = before + __shfl_sync(0xffffffffu, upto, src), in = (t - last + (sn + step - 1) / step) * step;
+        u.e = e0 + src;
+        u.row0 = s0 + in;
+        u.count = min(step, sn - in);
+        u.trow = group_tile_row(s0, u.e) + in / kTileRows;
+        u.off = in % kTileRows;
+        return u;
     }
-    return u;
-}
+};
 
 // two adjacent 16-bit outputs (4-byte aligned)
 template <typename TOut> __device__ __forceinline__ void store_pair(TOut *p, float a, float b)
@@ -248,9 +265,10 @@ __device__ __forceinline__ void write_columns(const float (&v)[32], float scale,
         TOut *y = Y + (int64_t)(row + odd) * ldy + n / 2;
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
+            if (i >= count) break;
             const float mine = (odd ? v[i + 1] : v[i]) * scale, give = (odd ? v[i] : v[i + 1]) * scale;
             const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-            const float a = odd ? silu_mul(got, mine) : silu_mul(mine, got);
+            const float a = silu_mul<TOut>(odd ? got : mine, odd ? mine : got);
             if (n < N && i + odd < count) store1<TOut>(y, a);
             y += 2 * ldy;
         }
@@ -258,6 +276,7 @@ __device__ __forceinline__ void write_columns(const float (&v)[32], float scale,
         TOut *y = Y + (int64_t)(row + odd) * ldy + (n & ~1);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
+            if (i >= count) break;
             const float mine = (odd ? v[i + 1] : v[i]) * scale, give = (odd ? v[i] : v[i + 1]) * scale;
             const float got = __shfl_xor_sync(0xffffffffu, give, 1);
             if (n < N && i + odd < count) store_pair<TOut>(y, odd ? got : mine, odd ? mine : got);
@@ -298,37 +317,36 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr)
 }
 
 // ---------------------------------------------------------------------------
-// mx_stream_kernel: few rows per group.  One CTA per 128 weight rows x up to
-// 128 activation rows: its time is the weights' way from HBM, so the ring of
-// stages is what matters: two CTAs share an SM, and a stage holds only as many
-// activation rows (in boxes of 32) as the unit has, so that few rows leave
-// room for more stages (5 of 22 KB for up to 32 rows, 3 of 34 KB for 128).
+// mx_stream_kernel: few rows per group.  A unit is 128 weight rows x up to 64
+// activation rows; its time is the weights' way from HBM, so what matters is
+// that copies never stop: two CTAs per SM, each a ring of stages that its
+// producer fills across the units the CTA takes in turn, while two
+// accumulators let the epilogue of one unit run beside the MMAs of the next.
 //   warp 0: bulk-tensor producer; warp 1: tensor memory, MMA issuer;
 //   warps 2-9: with TIn = void the epilogue alone, two warps per quarter of the
-//   accumulator's lanes; otherwise they first quantize the activations (TIn
+//   accumulator's lanes; otherwise they also quantize the activations (TIn
 //   [T, K]) to MXFP4, stage by stage, straight into the shared-memory operand
 //   and its scale tiles: a call with few rows is then one launch, reads X from
 //   L2 and needs no workspace.
-// Stage: 256 k of 128 weight rows (16 KB) and of the activation rows, and the
-// scale tiles of both.
+// Stage: 256 k of 128 weight rows (16 KB) and of `boxes` x 32 activation rows,
+// and the scale tiles of both: 5 stages of 22 KB, or 4 of 26 KB.
 // Where the units do not fill the SMs, the CTAs of a cluster share one: CTA z
 // takes part z of K, leaves its fp32 sums in its own shared memory, and after
 // a cluster barrier each CTA adds a share of the columns over the CTAs in
 // order (deterministic; no workspace, no second launch).
 // ---------------------------------------------------------------------------
 constexpr int kStreamWorkers = 8, kStreamThreads = 64 + 32 * kStreamWorkers;
-
-constexpr int kStreamRows = 128, kBoxRows = 32, kFuseRows = 16;
+constexpr int kStreamRows = 64, kBoxRows = 32, kFuseRows = 16;
 // two CTAs per SM: 227 KB / 2 less 1 KB each that the system keeps
 constexpr uint32_t kStreamRing = 115200u - 1024u - 512u, kStreamSmem = kStreamRing + 512u + 1024u;
 constexpr int kStreamMaxStages = 8;
 
 template <bool NV> struct StreamCfg {
     static constexpr uint32_t kA = 128 * 128, kBox = kBoxRows * 128, kS = kStepTiles<NV> * kTileBytes;
-    // tensor memory: accumulator, then the scales of a stage (weights, activations)
+    // tensor memory: two accumulators, then the scales of a stage (weights, activations)
     static constexpr uint32_t kScaleCols = kStepTiles<NV> * 4;
     static constexpr uint32_t kCols = 256;
-    static_assert(kStreamRows + 2 * kScaleCols <= kCols, "two CTAs share an SM's tensor memory");
+    static_assert(2 * kStreamRows + 2 * kScaleCols <= kCols, "two CTAs share an SM's tensor memory");
     static_assert(kStreamRing / (kA + kBox + 2 * kS) <= kStreamMaxStages, "barriers for every stage");
     static_assert(kStreamRing / (kA + kStreamRows * 128 + 2 * kS) >= 3, "a ring for the widest unit");
 };
@@ -338,7 +356,7 @@ template <bool NV, typename TOut, bool GATE, typename TIn>
 __global__ void __launch_bounds__(kStreamThreads, 2)
     mx_stream_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a,
                      const __grid_constant__ CUtensorMap tmap_sw, const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ Problem p,
-                     const TIn *__restrict__ X, int ntiles, int splits, TOut *__restrict__ Y, int inject_stall)
+                     const TIn *__restrict__ X, int ntiles, int splits, int boxes, TOut *__restrict__ Y, int inject_stall)
 {
     using Cfg = StreamCfg<NV>;
     constexpr bool kFused = !std::is_void<TIn>::value;
@@ -346,76 +364,71 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *bars = smem + kStreamRing;
-    const uint32_t full = smem_addr(bars), empty = full + 8 * kStreamMaxStages, acc_full = empty + 8 * kStreamMaxStages, drained = acc_full + 8;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * kStreamMaxStages, acc_full = empty + 8 * kStreamMaxStages, acc_empty = acc_full + 16,
+                   drained = acc_empty + 16;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + 256);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 260);
-    volatile int *unit_slot = reinterpret_cast<volatile int *>(bars + 264);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int z = splits > 1 ? (int)cluster_rank() : 0, block = blockIdx.x / (unsigned)splits;
-    const int n0 = block % ntiles * 128, t = block / ntiles;
+    const int z = splits > 1 ? (int)cluster_rank() : 0, block = blockIdx.x / (unsigned)splits, blocks = gridDim.x / (unsigned)splits;
     const int steps = (p.K + kStepK - 1) / kStepK;
-    // this CTA's stages: g0 .. g0 + nk - 1
-    const int g0 = (int)((int64_t)steps * z / splits), g1 = (int)((int64_t)steps * (z + 1) / splits);
+    // this CTA's stages of a unit: g0 .. g0 + nk - 1
+    const int g0 = (int)((int64_t)steps * z / splits), nk = (int)((int64_t)steps * (z + 1) / splits) - g0;
+    const uint32_t bbytes = (uint32_t)boxes * Cfg::kBox, stage = Cfg::kA + bbytes + 2 * Cfg::kS, stages = kStreamRing / stage;
 
     pdl_trigger();
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr((const void *)tmem_slot)),
-                     "n"(Cfg::kCols));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-        tc_fence_before();
-    }
     if (warp == 0) {
         // ---------------- producer ----------------
-        // It sets up the barriers itself and fills the ring before it meets the
-        // other warps: the first copies are on their way while they start.
+        // It sets up the barriers itself and does not wait for the other warps:
+        // the first copies are on their way while they start.
         const uint32_t lead = elect_one();
         if (lead) {
             for (int s = 0; s < kStreamMaxStages; s++) {
                 mbar_init(full + 8 * s, kFused ? 5 : 1);  // the producer, and the four warps that quantize the stage
                 mbar_init(empty + 8 * s, 1);
             }
-            mbar_init(acc_full, 1);
+            for (int b = 0; b < 2; b++) {
+                mbar_init(acc_full + 8 * b, 1);
+                mbar_init(acc_empty + 8 * b, kStreamWorkers);
+            }
             mbar_init(drained, 1);
             *abort_flag = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         __syncwarp();
+        asm volatile("barrier.cta.arrive 1, %0;" ::"n"(kStreamThreads) : "memory");
         pdl_wait();  // the operands may come from an earlier kernel of the stream
-        const RowUnit u = row_unit(p, t, kStreamRows);
-        if (lead) {
-            unit_slot[0] = u.e;
-            unit_slot[1] = u.row0;
-            unit_slot[2] = u.count;
-        }
-        const int nk = u.count > 0 ? g1 - g0 : 0, boxes = (u.count + kBoxRows - 1) / kBoxRows;
-        const uint32_t bbytes = (uint32_t)boxes * Cfg::kBox, stage = Cfg::kA + bbytes + 2 * Cfg::kS, stages = kStreamRing / stage;
-        const int wrow = u.e * p.N + n0, srow = u.e * p.trows_w + n0 / kTileRows;
         uint32_t s = 0, ph = 0;  // the ring: stage, how often it went round
-        bool ok = true;
-        if (nk <= 0) __syncthreads();
-        for (int g = 0; g < nk; g++) {
-            if (g >= (int)stages && !mbar_wait_all(empty + 8 * s, ph ^ 1u, abort_flag)) {
-                ok = false;
-                break;
-            }
-            // fault injection (tests only): the first CTA never fills its first stage
-            const bool stall = inject_stall && blockIdx.x == 0 && g == 0;
-            const uint32_t a0 = smem_addr(smem) + s * stage, f = full + 8 * s, s0 = a0 + Cfg::kA + bbytes;
-            const int c0 = (g0 + g) * 128, t0 = (g0 + g) * kStepTiles<NV> * 2;
-            if (lead && !stall) {
-                mbar_expect_tx(f, kFused ? Cfg::kA + Cfg::kS : stage);
-                tma_load_2d(a0, &tmap_w, c0, wrow, f);
-                tma_load_3d(s0, &tmap_sw, 0, t0, srow, f);
-                if constexpr (!kFused) {
-                    for (int b = 0; b < boxes; b++) tma_load_2d(a0 + Cfg::kA + b * Cfg::kBox, &tmap_a, c0, u.row0 + b * kBoxRows, f);
-                    tma_load_3d(s0 + Cfg::kS, &tmap_sa, 0, t0, u.trow, f);
+        bool ok = true, first = true;
+        RowWalk walk;
+        walk.begin(p, kStreamRows);
+        for (int u = block; ok; u += blocks) {
+            const RowUnit w = walk.at(p, u / ntiles, kStreamRows);
+            if (w.count <= 0) break;
+            const int n0 = u % ntiles * 128, wrow = w.e * p.N + n0, srow = w.e * p.trows_w + n0 / kTileRows;
+            for (int g = 0; g < nk; g++) {
+                if (!mbar_wait_all(empty + 8 * s, ph ^ 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                // fault injection (tests only): the first CTA never fills its first stage
+                const bool stall = inject_stall && blockIdx.x == 0 && first;
+                first = false;
+                const uint32_t a0 = smem_addr(smem) + s * stage, f = full + 8 * s, s0 = a0 + Cfg::kA + bbytes;
+                const int c0 = (g0 + g) * 128, t0 = (g0 + g) * kStepTiles<NV> * 2;
+                if (lead && !stall) {
+                    mbar_expect_tx(f, kFused ? Cfg::kA + Cfg::kS : stage);
+                    tma_load_2d(a0, &tmap_w, c0, wrow, f);
+                    tma_load_3d(s0, &tmap_sw, 0, t0, srow, f);
+                    if constexpr (!kFused) {
+                        for (int b = 0; b < boxes; b++) tma_load_2d(a0 + Cfg::kA + b * Cfg::kBox, &tmap_a, c0, w.row0 + b * kBoxRows, f);
+                        tma_load_3d(s0 + Cfg::kS, &tmap_sa, 0, t0, w.trow, f);
+                    }
+                }
+                if (++s == stages) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
-            if (++s == stages) {
-                s = 0;
-                ph ^= 1u;
-            }
-            if (g + 1 == min(nk, (int)stages)) __syncthreads();  // the ring is full, or all is on its way
         }
         if (!ok) {
             // loads already issued land within microseconds; their barriers may
@@ -425,27 +438,28 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             }
             __syncwarp();
         }
-    } else {
-        pdl_wait();
-        if (p.E > 0 && blockIdx.x == 0 && warp == 2) check_offsets(p.offsets, p.E, p.T);
-        __syncthreads();
-    }
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    const int ue = unit_slot[0], row0 = unit_slot[1], count = unit_slot[2], nk = count > 0 ? g1 - g0 : 0;
-    const uint32_t bbytes = (uint32_t)((count + kBoxRows - 1) / kBoxRows) * Cfg::kBox, stage = Cfg::kA + bbytes + 2 * Cfg::kS;
-    const uint32_t stages = kStreamRing / stage;
-
-    if (warp == 0) {
-        // done above
     } else if (warp == 1) {
-        if (nk > 0) {
-            // ---------------- MMA issuer ----------------
-            const uint32_t lead = elect_one();
-            const uint32_t idesc = idesc_fp4(NV, 128, (count + 7) & ~7);  // the MMA's width: a multiple of 8
-            const uint32_t sfa = tmem + kStreamRows, sfb = sfa + Cfg::kScaleCols;
-            uint32_t s = 0, ph = 0;
-            bool ok = true;
+        // ---------------- MMA issuer ----------------
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr((const void *)tmem_slot)),
+                     "n"(Cfg::kCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        tc_fence_before();
+        asm volatile("barrier.cta.sync 1, %0;" ::"n"(kStreamThreads) : "memory");
+        tc_fence_after();
+        pdl_wait();
+        const uint32_t lead = elect_one(), tmem = *tmem_slot, sfa = tmem + 2 * kStreamRows, sfb = sfa + Cfg::kScaleCols;
+        uint32_t s = 0, ph = 0, ti = 0;
+        bool ok = true;
+        RowWalk walk;
+        walk.begin(p, kStreamRows);
+        for (int u = block; ok; u += blocks, ti++) {
+            const RowUnit w = walk.at(p, u / ntiles, kStreamRows);
+            if (w.count <= 0) break;
+            const uint32_t b = ti & 1u, acc = tmem + b * kStreamRows;
+            // the epilogue has drained this accumulator
+            if (!mbar_wait_all(acc_empty + 8 * b, ((ti >> 1) & 1u) ^ 1u, abort_flag)) break;
+            const uint32_t idesc = idesc_fp4(NV, 128, (w.count + 7) & ~7);  // the MMA's width: a multiple of 8
+            const uint32_t off2 = kFused ? 0u : (uint32_t)w.off >> 5;
             for (int g = 0; g < nk; g++) {
                 if (!mbar_wait_all(full + 8 * s, ph, abort_flag)) {
                     ok = false;
@@ -454,88 +468,103 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
                 tc_fence_after();
                 const uint32_t a0 = smem_addr(smem) + s * stage, b0 = a0 + Cfg::kA, s0 = b0 + bbytes;
                 issue_scales<NV, false, 1>(lead, s0, s0 + Cfg::kS, sfa, sfb);
-                issue_mmas<NV, false, 1>(lead, tmem, a0, b0, sfa, sfb, 0u, idesc, g == 0);
+                issue_mmas<NV, false, 1>(lead, acc, a0, b0, sfa, sfb, off2, idesc, g == 0);
                 commit<false>(lead, empty + 8 * s);
                 if (++s == stages) {
                     s = 0;
                     ph ^= 1u;
                 }
             }
-            if (ok) commit<false>(lead, acc_full);
-            // every MMA issued has completed before the tensor memory is freed (bounded)
-            commit<false>(lead, drained);
-            const uint64_t t0 = globaltimer();
-            while (!mbar_try_wait(drained, 0) && globaltimer() - t0 < kTimeoutNs) {
-            }
-            __syncwarp();
+            if (ok) commit<false>(lead, acc_full + 8 * b);
         }
+        // every MMA issued has completed before the tensor memory is freed (bounded)
+        commit<false>(lead, drained);
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(drained, 0) && globaltimer() - t0 < kTimeoutNs) {
+        }
+        __syncwarp();
     } else {
-        bool ok = true;
-        if constexpr (kFused) {
-            // ---------------- quantizer ----------------
-            // Warps 2-5 take the even stages, 6-9 the odd ones, a thread one block
-            // of 32 at a time (16 rows are one block each); the block of the next
-            // stage is on its way while this one is encoded.  (Two stages in turn:
-            // a warp that took every fourth could be two rounds of the ring ahead,
-            // which a barrier's parity cannot tell from none.)
-            const int group = (warp - 2) >> 2, tid = (threadIdx.x - 64) & 127;
-            uint4 v[4];
-            auto load = [&](int g, int i) {
-                const int r = i >> 3, k = (g0 + g) * kStepK + 32 * (i & 7);
-                const bool in = g < nk && i < count * 8 && k < p.K;  // past K: zeros
-                const uint4 *x = reinterpret_cast<const uint4 *>(X + (int64_t)(row0 + r) * p.K + k);
+        asm volatile("barrier.cta.sync 1, %0;" ::"n"(kStreamThreads) : "memory");
+        tc_fence_after();
+        pdl_wait();
+        if (p.E > 0 && blockIdx.x == 0 && warp == 2) check_offsets(p.offsets, p.E, p.T);
+        const uint32_t tmem = *tmem_slot;
+        // ---------------- quantizer (of the unit with this CTA's number ti) ----------------
+        // Warps 2-5 take the even stages, 6-9 the odd ones, a thread one block of
+        // 32 at a time (16 rows are one block each); the block of the next stage
+        // is on its way while this one is encoded.  (Two stages in turn: a warp
+        // that took every fourth could be two rounds of the ring ahead, which a
+        // barrier's parity cannot tell from none.)
+        auto quantize = [&](const RowUnit &w, uint32_t ti) -> bool {
+            if constexpr (kFused) {
+                const int group = (warp - 2) >> 2, tid = (threadIdx.x - 64) & 127;
+                uint4 v[4];
+                auto load = [&](int g, int i) {
+                    const int r = i >> 3, k = (g0 + g) * kStepK + 32 * (i & 7);
+                    const bool in = g < nk && i < w.count * 8 && k < p.K;  // past K: zeros
+                    const uint4 *x = reinterpret_cast<const uint4 *>(X + (int64_t)(w.row0 + r) * p.K + k);
 #pragma unroll
-                for (int j = 0; j < 4; j++) v[j] = in ? __ldg(x + j) : make_uint4(0u, 0u, 0u, 0u);
-            };
-            load(group, tid);
-            uint32_t s = (uint32_t)group, ph = 0;
-            for (int g = group; g < nk; g += 2) {
-                if (!mbar_wait_all(empty + 8 * s, ph ^ 1u, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t *b0 = smem + s * stage + Cfg::kA, *sb = b0 + bbytes + Cfg::kS;
-                // 8 blocks a row: a block's 16 bytes of codes are one unit of the swizzle
-                for (int i = tid; i < count * 8; i += 128) {
-                    const int r = i >> 3, c = i & 7;
-                    uint4 codes;
-                    const unsigned byte = encode_block<TIn>(v, codes);
-                    load(i + 128 < count * 8 ? g : g + 2, i + 128 < count * 8 ? i + 128 : tid);
-                    *reinterpret_cast<uint4 *>(b0 + r * 128 + ((c ^ (r & 7)) << 4)) = codes;
-                    sb[(c >> 2) * kTileBytes + (r & 31) * 16 + (r >> 5) * 4 + (c & 3)] = (uint8_t)byte;
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full + 8 * s);
-                s += 2;
-                if (s >= stages) {
-                    s -= stages;
-                    ph ^= 1u;
+                    for (int j = 0; j < 4; j++) v[j] = in ? __ldg(x + j) : make_uint4(0u, 0u, 0u, 0u);
+                };
+                const uint32_t base = ti * (uint32_t)nk;  // stages before this unit
+                int g = (int)((base + (uint32_t)group) & 1u);
+                load(g, tid);
+                for (; g < nk; g += 2) {
+                    const uint32_t s = (base + (uint32_t)g) % stages, ph = ((base + (uint32_t)g) / stages) & 1u;
+                    if (!mbar_wait_all(empty + 8 * s, ph ^ 1u, abort_flag)) return false;
+                    uint8_t *b0 = smem + s * stage + Cfg::kA, *sb = b0 + bbytes + Cfg::kS;
+                    // 8 blocks a row: a block's 16 bytes of codes are one unit of the swizzle
+                    for (int i = tid; i < w.count * 8; i += 128) {
+                        const int r = i >> 3, c = i & 7;
+                        uint4 codes;
+                        const unsigned byte = encode_block<TIn>(v, codes);
+                        load(i + 128 < w.count * 8 ? g : g + 2, i + 128 < w.count * 8 ? i + 128 : tid);
+                        *reinterpret_cast<uint4 *>(b0 + r * 128 + ((c ^ (r & 7)) << 4)) = codes;
+                        sb[(c >> 2) * kTileBytes + (r & 31) * 16 + (r >> 5) * 4 + (c & 3)] = (uint8_t)byte;
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full + 8 * s);
                 }
             }
-        }
+            return true;
+        };
         // ---------------- epilogue ----------------
-        if (nk > 0 && ok && mbar_wait_warp(acc_full, 0, abort_flag)) {
+        const int q = warp & 3, c_first = ((warp - 2) >> 2) * 32, r = q * 32 + lane;  // quarter of the lanes; which of the columns
+        const int64_t ldy = GATE ? p.N / 2 : p.N;
+        const float ts_a = p.ts_a ? *p.ts_a : 1.0f;
+        uint32_t ti = 0;
+        RowWalk walk;
+        walk.begin(p, kStreamRows);
+        RowUnit w = walk.at(p, block / ntiles, kStreamRows);
+        bool ok = w.count <= 0 || quantize(w, 0);
+        for (int u = block; ok && w.count > 0; u += blocks, ti++) {
+            // the next unit's stages are quantized before this one's sums are written:
+            // its MMAs need them, and only its successor's this accumulator
+            const RowUnit next = walk.at(p, (u + blocks) / ntiles, kStreamRows);
+            if (next.count > 0 && !quantize(next, ti + 1)) break;
+            const uint32_t b = ti & 1u;
+            if (!mbar_wait_warp(acc_full + 8 * b, (ti >> 1) & 1u, abort_flag)) break;
             tc_fence_after();
-            const int q = warp & 3, r = q * 32 + lane;  // the quarter of the lanes this warp may read
-            float scale = 1.0f;
-            if (p.ts_a) scale = __fmul_rn(scale, *p.ts_a);
-            if (p.ts_w) scale = __fmul_rn(scale, p.ts_w[ue]);
-            const int64_t ldy = GATE ? p.N / 2 : p.N;
-#pragma unroll 1
-            for (int c0 = ((warp - 2) >> 2) * 32; c0 < count; c0 += 64) {
-                float v[32];
-                tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0, v);
+            const int n = u % ntiles * 128 + r;
+            const float scale = p.ts_w ? __fmul_rn(ts_a, p.ts_w[w.e]) : ts_a;
+            float v[32];
+            if (c_first < w.count) tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + b * kStreamRows + (uint32_t)c_first, v);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty + 8 * b);  // this warp has read its part: the accumulator goes back
+            if (c_first < w.count) {
                 if (splits == 1) {
-                    write_columns<TOut, GATE>(v, scale, p.N, Y, ldy, row0 + c0, count - c0, n0 + r, lane);
+                    write_columns<TOut, GATE>(v, scale, p.N, Y, ldy, w.row0 + c_first, w.count - c_first, n, lane);
                 } else {
-                    // the ring is free: every stage has been read by the MMAs
-                    float *part = reinterpret_cast<float *>(smem) + c0 * 128 + r;
+                    // the ring is free: the CTA's only unit has been read by its MMAs
+                    float *part = reinterpret_cast<float *>(smem) + c_first * 128 + r;
 #pragma unroll
                     for (int i = 0; i < 32; i++)
-                        if (c0 + i < count) part[i * 128] = v[i] * scale;
+                        if (c_first + i < w.count) part[i * 128] = v[i] * scale;
                 }
             }
+            w = next;
         }
         tc_fence_before();
     }
@@ -543,22 +572,25 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(Cfg::kCols));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tmem_slot), "n"(Cfg::kCols));
     }
     if (splits > 1) {
         cluster_sync();  // every CTA's sums are written
-        if (warp >= 2 && count > 0) {
-            const int w = warp - 2, q = w & 3, n = n0 + q * 32 + lane;
+        if (warp >= 2) {
+            RowWalk walk;
+            walk.begin(p, kStreamRows);
+            const RowUnit w = walk.at(p, block / ntiles, kStreamRows);
+            const int v = warp - 2, q = v & 3, n = block % ntiles * 128 + q * 32 + lane;
             const int64_t ldy = GATE ? p.N / 2 : p.N;
-            for (int c = z * 2 + (w >> 2); c < count; c += 2 * splits) {
+            for (int c = z * 2 + (v >> 2); c < w.count; c += 2 * splits) {
                 const uint32_t at = smem_addr(smem) + (uint32_t)(c * 128 + q * 32 + lane) * 4u;
                 float a = 0.0f;
                 for (int y = 0; y < splits; y++) a += ld_cluster(cluster_addr(at, (uint32_t)y));
                 if constexpr (GATE) {
                     const float up = __shfl_xor_sync(0xffffffffu, a, 1);
-                    if (n < p.N && !(lane & 1)) store1<TOut>(Y + (int64_t)(row0 + c) * ldy + n / 2, silu_mul(a, up));
+                    if (n < p.N && !(lane & 1)) store1<TOut>(Y + (int64_t)(w.row0 + c) * ldy + n / 2, silu_mul<TOut>(a, up));
                 } else {
-                    if (n < p.N) store1<TOut>(Y + (int64_t)(row0 + c) * ldy + n, a);
+                    if (n < p.N) store1<TOut>(Y + (int64_t)(w.row0 + c) * ldy + n, a);
                 }
             }
         }
@@ -669,8 +701,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint32_t lead = elect_one(), full0 = cluster_addr(full, 0);
         uint32_t s = 0, ph = 0;
         bool ok = true, first = true;
+        RowWalk walk;
+        walk.begin(p, step);
         for (int u = pair; ok; u += pairs) {
-            const RowUnit w = row_unit(p, u / ntiles, step);
+            const RowUnit w = walk.at(p, u / ntiles, step);
             if (w.count <= 0) break;
             const int n0 = (u % ntiles) * 256 + (int)rank * 128;
             const int arow = w.row0 + (int)rank * (((w.count + 15) & ~15) / 2);  // each CTA holds half of the unit's rows
@@ -721,8 +755,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             // this one, or two stages' at once, measured 10% slower.
             uint32_t s = 0, ph = 0, ti = 0;
             bool ok = true;
+            RowWalk walk;
+            walk.begin(p, step);
             for (int u = pair; ok; u += pairs, ti++) {
-                const RowUnit w = row_unit(p, u / ntiles, step);
+                const RowUnit w = walk.at(p, u / ntiles, step);
                 if (w.count <= 0) break;
                 const uint32_t b = ti & 1u, acc = tmem + b * kPairRows;
                 // the epilogue has drained this accumulator
@@ -762,8 +798,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int64_t ldy = GATE ? p.N / 2 : p.N;
         const float ts_a = p.ts_a ? *p.ts_a : 1.0f;
         uint32_t ti = 0;
+        RowWalk walk;
+        walk.begin(p, step);
         for (int u = pair;; u += pairs, ti++) {
-            const RowUnit w = row_unit(p, u / ntiles, step);
+            const RowUnit w = walk.at(p, u / ntiles, step);
             if (w.count <= 0) break;
             const uint32_t b = ti & 1u;
             if (!mbar_wait_warp(acc_full + 8 * b, (ti >> 1) & 1u, abort_flag)) break;
@@ -870,11 +908,14 @@ static razer_status launch_stream(const TIn *X, const uint8_t *codes_a, const ui
     }
     const int ntiles = (p.N + 127) / 128;
     const int64_t units = max_pieces(p.T, p.E, kStreamRows) * ntiles;
+    if (units > INT32_MAX - 1024) return RAZER_ERR_SHAPE;
     const int S = stream_splits(units, (p.K + kStepK - 1) / kStepK);
-    if (units * S > INT32_MAX) return RAZER_ERR_SHAPE;
+    // one CTA (or cluster) a unit, or where they are more, two CTAs an SM that take several
+    const int64_t grid = S > 1 ? units * S : std::min<int64_t>(units, 2 * (int64_t)sm_count());
+    const int boxes = p.T <= kBoxRows ? 1 : kStreamRows / kBoxRows;
     const int inject = fault_injection_enabled() ? 1 : 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * S));
+    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kStreamThreads);
     cfg.dynamicSmemBytes = kStreamSmem;
     cfg.stream = st;
@@ -886,7 +927,7 @@ static razer_status launch_stream(const TIn *X, const uint8_t *codes_a, const ui
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = S > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, mx_stream_kernel<NV, TOut, GATE, TIn>, mw, ma, msw, msa, p, X, ntiles, S, Y, inject) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, mx_stream_kernel<NV, TOut, GATE, TIn>, mw, ma, msw, msa, p, X, ntiles, S, boxes, Y, inject) != cudaSuccess)
         return RAZER_ERR_CUDA;
     return RAZER_OK;
 }
