@@ -8,6 +8,7 @@ an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -410,14 +411,19 @@ def _mx_shape(fn: str, name: str, t, shape, dtype, dev):
     return t
 
 
+_U8 = torch.uint8
+# torch.cuda.current_stream() builds an object, 3 us: as much as a launch
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _mx_call(fn: str, call, dev, stream, *args):
     """Calls the library with dev current and, without a stream, on dev's current stream."""
-    if dev.index != torch.cuda.current_device():
+    index = dev.index
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _mx_call(fn, call, dev, stream, *args)
-    # the raw handle: torch.cuda.current_stream() costs 3 us, as much as a launch
-    st = call(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream)
-    if st != RAZER_OK:
+    st = call(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if st:
         raise RazerError(fn, st)
 
 
@@ -426,10 +432,11 @@ def _mx_ptr(t):
 
 
 def _mx_matrix(fn: str, name: str, x, dims: int = 2):
-    if x.dim() != dims or not x.is_cuda or not x.is_contiguous():
+    shape = x.shape
+    if len(shape) != dims or not x.is_cuda or not x.is_contiguous():
         raise ValueError(f"{fn}: {name} must be a contiguous {dims}-dimensional CUDA tensor, got {tuple(x.shape)} on {x.device}"
                          f"{'' if x.is_contiguous() else ', not contiguous'}")
-    return x.shape
+    return shape
 
 
 def _mx_groups(fn: str, offsets, dev) -> int:
@@ -462,10 +469,10 @@ def razer_quantize_mx(X: torch.Tensor, offsets: torch.Tensor | None = None, *, c
     fn = "razer_quantize_mx"
     M, K = _mx_matrix(fn, "X", X)
     dev = X.device
-    E = _mx_groups(fn, offsets, dev)
+    E = 0 if offsets is None else _mx_groups(fn, offsets, dev)
     r, c, b = shape = _mx_tiles(M, K, 32, E)
-    codes = torch.empty(M, K // 2, dtype=torch.uint8, device=dev) if codes is None else _mx_shape(fn, "codes", codes, (M, K // 2), torch.uint8, dev)
-    scales = torch.empty(r, c, b, dtype=torch.uint8, device=dev) if scales is None else _mx_shape(fn, "scales", scales, shape, torch.uint8, dev)
+    codes = torch.empty(M, K // 2, dtype=_U8, device=dev) if codes is None else _mx_shape(fn, "codes", codes, (M, K // 2), _U8, dev)
+    scales = torch.empty(r, c, b, dtype=_U8, device=dev) if scales is None else _mx_shape(fn, "scales", scales, shape, _U8, dev)
     _mx_call(fn, load().razer_quantize_mx, dev, stream, X.data_ptr(), _DT.get(X.dtype, -1), M, K, _mx_ptr(offsets), E, codes.data_ptr(),
              scales.data_ptr())
     return codes, scales
@@ -477,9 +484,9 @@ def razer_dequant_mx(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torch.
     fn = "razer_dequant_mx"
     M, K2 = shape = _mx_matrix(fn, "codes", codes)
     dev, K = codes.device, 2 * K2
-    E = _mx_groups(fn, offsets, dev)
-    _mx_shape(fn, "codes", codes, shape, torch.uint8, dev)
-    _mx_shape(fn, "scales", scales, _mx_tiles(M, K, 32, E), torch.uint8, dev)
+    E = 0 if offsets is None else _mx_groups(fn, offsets, dev)
+    _mx_shape(fn, "codes", codes, shape, _U8, dev)
+    _mx_shape(fn, "scales", scales, _mx_tiles(M, K, 32, E), _U8, dev)
     out = torch.empty(M, K, dtype=out_dtype, device=dev) if out is None else _mx_shape(fn, "out", out, (M, K), out.dtype, dev)
     _mx_call(fn, load().razer_dequant_mx, dev, stream, codes.data_ptr(), scales.data_ptr(), M, K, _mx_ptr(offsets), E, out.data_ptr(),
              _DT.get(out.dtype, -1))
@@ -513,12 +520,12 @@ def _mx_act(fn: str, act) -> int:
 def _mx_weights(fn: str, codes_w, scales_w, E: int, K: int, block: int, dev, ts_w=None) -> int:
     """Checks packed weights [N, K/2], or [E, N, K/2] for row groups; returns N."""
     shape = codes_w.shape
-    if len(shape) != (3 if E else 2):
-        raise ValueError(f"{fn}: codes_w must be {'[E, N, K/2]' if E else '[N, K/2]'}, got {tuple(shape)}")
+    if len(shape) != (3 if E else 2) or shape[-1] != K // 2 or (E and shape[0] != E):
+        raise ValueError(f"{fn}: codes_w must be {f'[{E}, N, {K // 2}]' if E else f'[N, {K // 2}]'}, got {tuple(shape)}")
     N = shape[-2]
-    _mx_shape(fn, "codes_w", codes_w, (E, N, K // 2) if E else (N, K // 2), torch.uint8, dev)
-    tiles = _mx_tiles(N, K, block)
-    _mx_shape(fn, "scales_w", scales_w, (E, *tiles) if E else tiles, torch.uint8, dev)
+    _mx_shape(fn, "codes_w", codes_w, shape, _U8, dev)
+    tiles = (-(-N // 128), -(-K // (4 * block)), 512)
+    _mx_shape(fn, "scales_w", scales_w, (E, *tiles) if E else tiles, _U8, dev)
     if ts_w is not None:
         _mx_shape(fn, "ts_w", ts_w, (E or 1,), torch.float32, dev)
     return N
@@ -569,24 +576,31 @@ def razer_gemm_mx_grouped(codes_a: torch.Tensor, scales_a: torch.Tensor, offsets
                        ts_w, act, out, stream)
 
 
+@functools.lru_cache(maxsize=1024)
+def razer_gemm_mx_grouped_workspace_size(T: int, K: int, groups: int) -> int:
+    """Workspace bytes of razer_gemm_mx_grouped_online (groups = 0: of razer_gemm_mx_online)."""
+    return int(load().razer_gemm_mx_grouped_workspace_size(T, K, groups))
+
+
 def _mx_online(fn, call, X, offsets, codes_w, scales_w, out_dtype, act, out, workspace, stream):
     T, K = _mx_matrix(fn, "X", X)
     dev = X.device
-    E, a = _mx_groups(fn, offsets, dev), _mx_act(fn, act)
+    E = 0 if offsets is None else _mx_groups(fn, offsets, dev)
+    a = _mx_act(fn, act) if act else 0
     N = _mx_weights(fn, codes_w, scales_w, E, K, 32, dev)
     out = _mx_out(fn, out, T, N, a, out_dtype, dev, E)
     if workspace is None:
-        need = load().razer_gemm_mx_grouped_workspace_size(T, K, E)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws = need
+        ws, wp = razer_gemm_mx_grouped_workspace_size(T, K, E), None
+        if ws:
+            workspace = torch.empty(ws, dtype=_U8, device=dev)
+            wp = workspace.data_ptr()
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"{fn}: workspace must be a contiguous tensor on {dev}")
     else:
-        ws = workspace.numel() * workspace.element_size()
+        ws, wp = workspace.numel() * workspace.element_size(), workspace.data_ptr()
     groups = (offsets.data_ptr(), E) if E else ()
     _mx_call(fn, call, dev, stream, X.data_ptr(), _DT.get(X.dtype, -1), T, *groups, codes_w.data_ptr(), scales_w.data_ptr(), N, K, a,
-             out.data_ptr(), _DT.get(out.dtype, -1), _mx_ptr(workspace), ws)
+             out.data_ptr(), _DT.get(out.dtype, -1), wp, ws)
     return out
 
 
@@ -604,11 +618,6 @@ def razer_gemm_mx_grouped_online(X: torch.Tensor, offsets: torch.Tensor, codes_w
         raise ValueError("razer_gemm_mx_grouped_online: offsets are needed")
     return _mx_online("razer_gemm_mx_grouped_online", load().razer_gemm_mx_grouped_online, X, offsets, codes_w, scales_w, out_dtype, act, out,
                       workspace, stream)
-
-
-def razer_gemm_mx_grouped_workspace_size(T: int, K: int, groups: int) -> int:
-    """Workspace bytes of razer_gemm_mx_grouped_online."""
-    return int(load().razer_gemm_mx_grouped_workspace_size(T, K, groups))
 
 
 def razer_get_device_status(stream=None) -> int:
