@@ -77,21 +77,43 @@ template <typename T> __device__ __forceinline__ unsigned encode_block(const uin
 // a / b for a >= 0: the 64-bit division costs as much as encoding 16 values
 __device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) { return a <= UINT32_MAX ? (uint32_t)a / (uint32_t)b : a / b; }
 
-// Where the scales of row `row` start in their tile row; NULL: a row of no
-// group, left as it is.
-__device__ __forceinline__ uint8_t *row_tiles(int64_t row, int64_t M, int64_t ct, const int32_t *offsets, int E, const uint8_t *tiles)
+// The offsets of up to kEdges - 1 groups in shared memory, where a search is
+// cheap (through global memory it took half as long again as the quantizing);
+// more stay where they are.
+constexpr int kEdges = 256;
+__device__ __forceinline__ const int32_t *stage_edges(const int32_t *offsets, int E, int32_t (&edges)[kEdges])
 {
-    int64_t trow = row / kTileRows;
-    int in_tile = (int)(row % kTileRows);
-    if (E > 0) {
-        const int e = group_of_row(offsets, E, (int)M, (int)row);
-        if (e < 0) return nullptr;
-        const int start = group_edge(offsets, e, (int)M), i = (int)row - start;
-        trow = group_tile_row(start, e) + i / kTileRows;
-        in_tile = i % kTileRows;
-    }
-    return const_cast<uint8_t *>(tiles) + trow * ct * kTileBytes + (in_tile & 31) * 16 + (in_tile >> 5) * 4;
+    if (E == 0 || E >= kEdges) return offsets;
+    for (int i = threadIdx.x; i <= E; i += blockDim.x) edges[i] = offsets[i];
+    __syncthreads();
+    return edges;
 }
+
+// Finds where the scales of a row start in their tile row; NULL: a row of no
+// group, left as it is.  A thread keeps the group it met last.
+struct RowTiles {
+    int e, start, end;
+    __device__ __forceinline__ uint8_t *at(int64_t row, int64_t M, int64_t ct, const int32_t *offsets, int E, const uint8_t *tiles)
+    {
+        int64_t trow = row / kTileRows;
+        int in_tile = (int)(row % kTileRows);
+        if (E > 0) {
+            const int r = (int)row;
+            if (r < start || r >= end) {
+                e = group_of_row(offsets, E, (int)M, r);
+                if (e < 0) {
+                    start = end = 0;
+                    return nullptr;
+                }
+                start = group_edge(offsets, e, (int)M);
+                end = group_edge(offsets, e + 1, (int)M);
+            }
+            trow = group_tile_row(start, e) + (r - start) / kTileRows;
+            in_tile = (r - start) % kTileRows;
+        }
+        return const_cast<uint8_t *>(tiles) + trow * ct * kTileBytes + (in_tile & 31) * 16 + (in_tile >> 5) * 4;
+    }
+};
 
 // One lane per block of 32, 32 consecutive blocks of the matrix per warp and
 // task: no shuffles for the largest magnitude, 16 bytes of codes a lane, half
@@ -107,10 +129,11 @@ constexpr int kQuantizeCtas = 4, kRing = 2;  // CTAs per SM: one wave
 
 template <typename T>
 __global__ void __launch_bounds__(256, kQuantizeCtas) quantize_mx_kernel(const T *__restrict__ x, int64_t M, int64_t K,
-                                                                         const int32_t *__restrict__ offsets, int E,
+                                                                         const int32_t *offsets, int E,
                                                                          uint8_t *__restrict__ codes, uint8_t *__restrict__ tiles)
 {
     __shared__ uint4 ring[8][kRing][128];
+    __shared__ int32_t edges[kEdges];
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31;
@@ -119,6 +142,7 @@ __global__ void __launch_bounds__(256, kQuantizeCtas) quantize_mx_kernel(const T
     const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
     const int64_t kb = K / 32, ct = tile_cols(false, K), nb = M * kb;
     if (E > 0 && blockIdx.x == 0 && threadIdx.x < 32) check_offsets(offsets, E, (int)M);
+    offsets = stage_edges(offsets, E, edges);
     auto fetch = [&](int64_t task, int slot) {
         const uint4 *src = reinterpret_cast<const uint4 *>(x) + task * 128;
 #pragma unroll
@@ -130,6 +154,7 @@ __global__ void __launch_bounds__(256, kQuantizeCtas) quantize_mx_kernel(const T
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    RowTiles rt = {0, 0, 0};
     int slot = 0;
 #pragma unroll
     for (int i = 0; i < kRing - 1; i++) fetch(warp + i * warps, i);
@@ -137,7 +162,7 @@ __global__ void __launch_bounds__(256, kQuantizeCtas) quantize_mx_kernel(const T
         fetch(task + (kRing - 1) * warps, slot == 0 ? kRing - 1 : slot - 1);
         const int64_t blk = task * 32 + lane, row = div_small(blk, kb);
         const int c = (int)(blk - row * kb);
-        uint8_t *t = blk < nb ? row_tiles(row, M, ct, offsets, E, tiles) : nullptr;
+        uint8_t *t = blk < nb ? rt.at(row, M, ct, offsets, E, tiles) : nullptr;
         asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
         __syncwarp();
         uint4 v[4], out;
@@ -186,9 +211,10 @@ constexpr int kTaskCols = 1024;  // columns of one row that a warp takes at a ti
 
 template <typename TOut>
 __global__ void __launch_bounds__(256) dequant_mx_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ tiles, int64_t M,
-                                                         int64_t K, int64_t chunks, const int32_t *__restrict__ offsets, int E,
+                                                         int64_t K, int64_t chunks, const int32_t *offsets, int E,
                                                          TOut *__restrict__ out)
 {
+    __shared__ int32_t edges[kEdges];
     pdl_trigger();
     pdl_wait();
     constexpr int kPer = 16 / (int)sizeof(TOut), kIters = kTaskCols / (32 * kPer);
@@ -197,10 +223,12 @@ __global__ void __launch_bounds__(256) dequant_mx_kernel(const uint8_t *__restri
     const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
     const int64_t ct = tile_cols(false, K), total = M * chunks;
     if (E > 0 && blockIdx.x == 0 && threadIdx.x < 32) check_offsets(offsets, E, (int)M);
+    offsets = stage_edges(offsets, E, edges);
+    RowTiles rt = {0, 0, 0};
     for (int64_t task = warp; task < total; task += warps) {
         const int64_t row = div_small(task, chunks);
         const int col = (int)(task - row * chunks) * kTaskCols;
-        const uint8_t *scales = row_tiles(row, M, ct, offsets, E, tiles);
+        const uint8_t *scales = rt.at(row, M, ct, offsets, E, tiles);
         if (!scales) continue;
         unsigned w[kIters], sb[kIters];
 #pragma unroll

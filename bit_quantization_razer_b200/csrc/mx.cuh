@@ -34,7 +34,7 @@ __host__ __device__ constexpr int64_t tile_rows_grouped(int64_t T, int64_t E) { 
 // beyond T) reads and writes inside the buffers all the same
 __device__ __forceinline__ int group_edge(const int32_t *offsets, int i, int T)
 {
-    const int v = __ldg(offsets + i);
+    const int v = offsets[i];
     return v < 0 ? 0 : (v > T ? T : v);
 }
 // reports offsets that break the rules in the device status word (one warp of a launch calls it)

@@ -52,6 +52,24 @@ __device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity, vol
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
 }
 
+// Whether the phase is over, without waiting: asked a stage ahead, so that the
+// answer's latency (some 80 cycles) passes beside the instructions issued
+// meanwhile.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+// ... and the wait for it: `ready` is mbar_test's answer
+__device__ __forceinline__ bool mbar_wait_tested(bool ready, uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    return __all_sync(0xffffffffu, ready) || mbar_wait_all(bar, parity, abort_flag);
+}
+
 // Shared-memory descriptors, the two 32-bit halves apart: codes (K-major,
 // 128-byte swizzle, 8-row groups 1024 bytes apart) and one scale tile (32 rows
 // of 16 bytes, no swizzle, 8-row groups 128 bytes apart).
@@ -252,44 +270,60 @@ template <typename TOut> __device__ __forceinline__ void store_pair(TOut *p, flo
 // the rows row .. row + count - 1 (at most 32).  Adjacent lanes swap halves of
 // two columns, so that the even lane finishes the first row and the odd lane
 // the second: a gated pair meets in one lane and every lane computes one, and
-// 16-bit outputs leave in pairs, 16 stores instead of 32.  (One store per
-// column and lane, the gate tested inside the loop: 15,700 cycles for a unit
-// of 192 rows, twice what its 16 stages of MMAs take.)
+// 16-bit outputs leave in pairs, 16 stores instead of 32.  ALL: 32 rows; the
+// 16 chains are then free of branches and run into each other (with a test
+// between them a unit of 192 rows took 7,000 cycles, longer than its 16 stages
+// of MMAs; with one store per column and lane and the gate tested inside the
+// loop 15,700).
+template <typename TOut, bool GATE, bool ALL>
+__device__ __forceinline__ void write_columns_n(const float (&v)[32], float scale, TOut *__restrict__ Y, int64_t ldy, int count, bool mine, int lane)
+{
+    const int odd = lane & 1;
+    if constexpr (GATE || sizeof(TOut) == 2) {
+        // two rows a step
+        TOut *y = Y + (odd ? ldy : 0);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            if (!ALL && i >= count) break;
+            const float keep = (odd ? v[i + 1] : v[i]) * scale, give = (odd ? v[i] : v[i + 1]) * scale;
+            const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+            const float even = odd ? got : keep, next = odd ? keep : got;  // columns n & ~1 and n | 1
+            if (mine && (ALL || i + odd < count)) {
+                if constexpr (GATE) store1<TOut>(y, silu_mul<TOut>(even, next));  // row 2j of the weights gates row 2j + 1
+                else store_pair<TOut>(y, even, next);
+            }
+            y += 2 * ldy;
+        }
+    } else {
+        TOut *y = Y;
+#pragma unroll
+        for (int i = 0; i < 32; i++) {
+            if (!ALL && i >= count) break;
+            if (mine) store1<TOut>(y, v[i] * scale);
+            y += ldy;
+        }
+    }
+}
 template <typename TOut, bool GATE>
 __device__ __forceinline__ void write_columns(const float (&v)[32], float scale, int N, TOut *__restrict__ Y, int64_t ldy, int row, int count,
                                               int n, int lane)
 {
-    const int odd = lane & 1;
-    if constexpr (GATE) {
-        // row 2j of the weights gates row 2j + 1
-        TOut *y = Y + (int64_t)(row + odd) * ldy + n / 2;
+    const bool mine = n < N;
+    TOut *y = Y + (int64_t)row * ldy;
+    if constexpr (!GATE && sizeof(TOut) == 2) {
+        if (ldy & 1) {  // rows of an odd length: no pairs
+            y += n;
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            if (i >= count) break;
-            const float mine = (odd ? v[i + 1] : v[i]) * scale, give = (odd ? v[i] : v[i + 1]) * scale;
-            const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-            const float a = silu_mul<TOut>(odd ? got : mine, odd ? mine : got);
-            if (n < N && i + odd < count) store1<TOut>(y, a);
-            y += 2 * ldy;
-        }
-    } else if (sizeof(TOut) == 2 && (ldy & 1) == 0) {
-        TOut *y = Y + (int64_t)(row + odd) * ldy + (n & ~1);
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            if (i >= count) break;
-            const float mine = (odd ? v[i + 1] : v[i]) * scale, give = (odd ? v[i] : v[i + 1]) * scale;
-            const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-            if (n < N && i + odd < count) store_pair<TOut>(y, odd ? got : mine, odd ? mine : got);
-            y += 2 * ldy;
-        }
-    } else {
-        TOut *y = Y + (int64_t)row * ldy + n;
-#pragma unroll
-        for (int i = 0; i < 32; i++) {
-            if (n < N && i < count) store1<TOut>(y, v[i] * scale);
-            y += ldy;
+            for (int i = 0; i < 32; i++) {
+                if (mine && i < count) store1<TOut>(y, v[i] * scale);
+                y += ldy;
+            }
+            return;
         }
     }
+    y += GATE ? n / 2 : (sizeof(TOut) == 2 ? n & ~1 : n);
+    if (count >= 32) write_columns_n<TOut, GATE, true>(v, scale, y, ldy, count, mine, lane);
+    else write_columns_n<TOut, GATE, false>(v, scale, y, ldy, count, mine, lane);
 }
 
 // shared-memory address of the same object in CTA `rank` of the cluster
@@ -607,18 +641,19 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 // rows is what the FP4 rate asks for: an SM's operands per 256 k are (128 +
 // 96) x 128 bytes for 384 cycles of MMA, 75 bytes a cycle, where one CTA
 // alone would need 107.
-//   warps 0 and 10: bulk-tensor producers, weights and activations (each CTA
-//   loads its own operands; the leader's barrier counts both); one warp alone
-//   needs 390 cycles for a stage's four copies, as long as its MMAs take;
+//   warps 0 and 14: bulk-tensor producers, a stage in turn (each CTA loads its
+//   own operands; the leader's barrier counts both); one warp alone needs 390
+//   cycles for a stage's four copies, as long as its MMAs take;
 //   warp 1: tensor memory, and in the leader the MMA issuer;
-//   warps 2-9: epilogue, two warps per quarter of the lanes.
+//   warps 2-13: epilogue, three warps per quarter of the lanes: with two the
+//   last unit's, which nothing hides, took 5,300 cycles.
 // Two accumulators of 192 columns: the epilogue of a unit runs beside the MMAs
 // of the next.  384 + 24 (NVFP4: 48) columns of scales fit in 512; 256-wide
 // accumulators would leave no room for them.
 // A unit's rows start at a multiple of 64 rows of their group, so its scales
 // start at column 0 or 2 of their tile.
 // ---------------------------------------------------------------------------
-constexpr int kPairRows = 192, kPairEpiWarps = 8, kPairThreads = 96 + 32 * kPairEpiWarps;
+constexpr int kPairRows = 192, kPairEpiWarps = 12, kPairThreads = 96 + 32 * kPairEpiWarps;
 
 template <bool NV> struct PairCfg {
     static constexpr uint32_t kA = 128 * 128, kB = kPairRows / 2 * 128, kS = kStepTiles<NV> * kTileBytes;
@@ -630,9 +665,13 @@ template <bool NV> struct PairCfg {
     static_assert(16 * kStages + 40 <= 256, "barriers");
 };
 
+// An arrival on a barrier of either CTA that orders no memory: it says that
+// tensor memory has been read (tcgen05.wait::ld and the fence before it order
+// that).  As a release it waited for the warp's stores of the outputs, 2,000
+// to 3,000 cycles a unit.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // loads into this CTA's shared memory that count on a barrier of either CTA of the pair
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar)
@@ -653,8 +692,9 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
 template <bool NV, typename TOut, bool GATE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a,
-                   const __grid_constant__ CUtensorMap tmap_sw, const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ Problem p,
-                   int ntiles, int step, TOut *__restrict__ Y, int inject_stall)
+                   const __grid_constant__ CUtensorMap tmap_a64, const __grid_constant__ CUtensorMap tmap_a32,
+                   const __grid_constant__ CUtensorMap tmap_sw,
+                   const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ Problem p, int ntiles, int step, TOut *__restrict__ Y, int inject_stall)
 {
     using Cfg = PairCfg<NV>;
     constexpr int STAGES = Cfg::kStages;
@@ -699,41 +739,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (warp == 0 || warp == kPairEpiWarps + 2) {
         // ---------------- producers ----------------
         const uint32_t lead = elect_one(), full0 = cluster_addr(full, 0);
-        uint32_t s = 0, ph = 0;
-        bool ok = true, first = true;
+        // the two warps take the stages in turn
+        const uint32_t turn = warp == 0 ? 0u : 1u;
+        uint32_t s = turn, ph = 0, base = 0;  // base: stages before this unit
+        bool ok = true, ready = true;
         RowWalk walk;
         walk.begin(p, step);
-        for (int u = pair; ok; u += pairs) {
+        for (int u = pair; ok; u += pairs, base += (uint32_t)nk) {
             const RowUnit w = walk.at(p, u / ntiles, step);
             if (w.count <= 0) break;
             const int n0 = (u % ntiles) * 256 + (int)rank * 128;
-            const int arow = w.row0 + (int)rank * (((w.count + 15) & ~15) / 2);  // each CTA holds half of the unit's rows
+            const int half = ((w.count + 15) & ~15) / 2, arow = w.row0 + (int)rank * half;  // each CTA holds half of the unit's rows
+            // the box that holds them, in one copy (three boxes of 32 took a third longer than one of 96)
+            const CUtensorMap *tmap_act = half > 64 ? &tmap_a : half > 32 ? &tmap_a64 : &tmap_a32;
+            const uint32_t bytes = Cfg::kStage - Cfg::kB + (uint32_t)(half > 64 ? 96 : half > 32 ? 64 : 32) * 128u;
             const int wrow = w.e * p.N + n0;
             // a weight tile row that does not exist: any other will do, its rows are not written
             const int srow = w.e * p.trows_w + min(n0 / kTileRows, p.trows_w - 1);
-            for (int g = 0; g < nk; g++) {
-                if (!mbar_wait_all(empty + 8 * s, ph ^ 1u, abort_flag)) {
+            for (int g = (int)((base ^ turn) & 1u); g < nk; g += 2) {
+                const uint32_t e = empty + 8 * s, fl = full + 8 * s, f = full0 + 8 * s, a0 = smem_addr(smem) + s * Cfg::kStage,
+                               s0 = a0 + Cfg::kA + Cfg::kB, now = ph;
+                if (!mbar_wait_tested(ready, e, now ^ 1u, abort_flag)) {
                     ok = false;
                     break;
                 }
+                s += 2;
+                if (s >= STAGES) {
+                    s -= STAGES;
+                    ph ^= 1u;
+                }
+                ready = mbar_test(empty + 8 * s, ph ^ 1u);
                 // fault injection (tests only): the first CTA never fills its first stage
-                const bool stall = inject_stall && blockIdx.x == 0 && first;
-                first = false;
-                const uint32_t a0 = smem_addr(smem) + s * Cfg::kStage, f = full0 + 8 * s, s0 = a0 + Cfg::kA + Cfg::kB;
+                const bool stall = inject_stall && blockIdx.x == 0 && base == 0 && g == 0;
                 const int t0 = g * kStepTiles<NV> * 2;
                 if (lead && !stall) {
-                    if (warp == 0) {
-                        if (rank == 0) mbar_expect_tx(full + 8 * s, 2 * Cfg::kStage);
-                        tma_load_2d_pair(a0, &tmap_w, g * 128, wrow, f);
-                        tma_load_3d_pair(s0, &tmap_sw, 0, t0, srow, f);
-                    } else {
-                        tma_load_2d_pair(a0 + Cfg::kA, &tmap_a, g * 128, arow, f);
-                        tma_load_3d_pair(s0 + Cfg::kS, &tmap_sa, 0, t0, w.trow, f);
-                    }
-                }
-                if (++s == STAGES) {
-                    s = 0;
-                    ph ^= 1u;
+                    if (rank == 0) mbar_expect_tx(fl, 2 * bytes);
+                    tma_load_2d_pair(a0, &tmap_w, g * 128, wrow, f);
+                    tma_load_2d_pair(a0 + Cfg::kA, tmap_act, g * 128, arow, f);
+                    tma_load_3d_pair(s0, &tmap_sw, 0, t0, srow, f);
+                    tma_load_3d_pair(s0 + Cfg::kS, &tmap_sa, 0, t0, w.trow, f);
                 }
             }
         }
@@ -754,7 +798,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             // 384 of them MMAs.  Copying the next stage's scales between the MMAs of
             // this one, or two stages' at once, measured 10% slower.
             uint32_t s = 0, ph = 0, ti = 0;
-            bool ok = true;
+            bool ok = true, ready = false;
             RowWalk walk;
             walk.begin(p, step);
             for (int u = pair; ok; u += pairs, ti++) {
@@ -765,19 +809,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 if (!mbar_wait_all(acc_empty + 8 * b, ((ti >> 1) & 1u) ^ 1u, abort_flag)) break;
                 const uint32_t idesc = idesc_fp4(NV, 256, (w.count + 15) & ~15), off2 = (uint32_t)w.off >> 5;
                 for (int g = 0; g < nk; g++) {
-                    if (!mbar_wait_all(full + 8 * s, ph, abort_flag)) {
+                    if (!mbar_wait_tested(ready, full + 8 * s, ph, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a0 = smem_addr(smem) + s * Cfg::kStage, b0 = a0 + Cfg::kA, s0 = b0 + Cfg::kB;
-                    issue_scales<NV, true, 2>(lead, s0, s0 + Cfg::kS, sfa, sfb);
-                    issue_mmas<NV, true, 2>(lead, acc, a0, b0, sfa, sfb, off2, idesc, g == 0);
-                    commit<true>(lead, empty + 8 * s);
+                    const uint32_t a0 = smem_addr(smem) + s * Cfg::kStage, b0 = a0 + Cfg::kA, s0 = b0 + Cfg::kB, e = empty + 8 * s;
                     if (++s == STAGES) {
                         s = 0;
                         ph ^= 1u;
                     }
+                    ready = mbar_test(full + 8 * s, ph);
+                    issue_scales<NV, true, 2>(lead, s0, s0 + Cfg::kS, sfa, sfb);
+                    issue_mmas<NV, true, 2>(lead, acc, a0, b0, sfa, sfb, off2, idesc, g == 0);
+                    commit<true>(lead, e);
                 }
                 if (ok) commit<true>(lead, acc_full + 8 * b);
             }
@@ -793,7 +838,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
     } else {
         // ---------------- epilogue ----------------
-        const int q = warp & 3, c_first = ((warp - 2) >> 2) * 32;  // quarter of the lanes; which of each 64 columns
+        const int q = warp & 3, c_first = ((warp - 2) >> 2) * 32;  // quarter of the lanes; which of each 96 columns
         const uint32_t acc_empty0 = cluster_addr(acc_empty, 0);
         const int64_t ldy = GATE ? p.N / 2 : p.N;
         const float ts_a = p.ts_a ? *p.ts_a : 1.0f;
@@ -809,10 +854,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int n = (u % ntiles) * 256 + (int)rank * 128 + q * 32 + lane;
             const float scale = p.ts_w ? __fmul_rn(ts_a, p.ts_w[w.e]) : ts_a;
 #pragma unroll 1
-            for (int c0 = c_first; c0 < w.count || c0 == c_first; c0 += 64) {
+            for (int c0 = c_first; c0 < w.count || c0 == c_first; c0 += kPairEpiWarps * 8) {
                 float v[32];
                 tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + b * kPairRows + (uint32_t)c0, v);
-                if (c0 + 64 >= w.count) {
+                if (c0 + kPairEpiWarps * 8 >= w.count) {
                     // this warp has read its part of the accumulator: hand it back
                     tc_fence_before();
                     __syncwarp();
@@ -932,8 +977,30 @@ static razer_status launch_stream(const TIn *X, const uint8_t *codes_a, const ui
     return RAZER_OK;
 }
 
+static int64_t rows_per_group(int64_t T, int64_t E) { return E > 0 ? (T + E - 1) / E : T; }
+
+// Rows of a unit: 192, or fewer where smaller units need no more rounds over
+// the pairs of SMs.  A unit's time goes as 220 + rows (4096 x 4096, one round:
+// 8.7 / 9.6 / 10.4 us for 64 / 128 / 192 rows, 5 of them the launch); so 256
+// rows take 64 at a time (9.2 us, 192 at a time 10.4), 700 rows 192 (11.0;
+// 128: 13.7, 64: 16.8).
+static int pair_step(const Problem &p, int ntiles, int pairs)
+{
+    const int64_t E = p.E ? p.E : 1, rows = rows_per_group(p.T, p.E);
+    int best = kPairRows;
+    int64_t cost = INT64_MAX;
+    for (int step = kPairRows; step >= 64; step -= 64) {
+        const int64_t units = E * ((rows + step - 1) / step) * ntiles, c = (units + pairs - 1) / pairs * (220 + step);
+        if (c < cost) {
+            cost = c;
+            best = step;
+        }
+    }
+    return best;
+}
+
 template <bool NV, typename TOut, bool GATE>
-static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, int step, TOut *Y, cudaStream_t st)
+static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, TOut *Y, cudaStream_t st)
 {
     using Cfg = PairCfg<NV>;
     static int resident[64] = {0};  // clusters that the device holds at once
@@ -957,28 +1024,27 @@ static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, 
         pairs = std::min(pairs, sm_count() / 2);
         if (dev >= 0 && dev < 64) resident[dev] = pairs;
     }
-    CUtensorMap mw, ma, msw, msa;
+    CUtensorMap mw, ma, ma64, ma32, msw, msa;
     const int64_t E = p.E ? p.E : 1, arows = p.E ? tile_rows_grouped(p.T, p.E) : tile_rows(p.T);
     if (!encode_codes_map(&mw, codes_w, p.N * E, p.K, 128) || !encode_codes_map(&ma, codes_a, p.T, p.K, kPairRows / 2) ||
+        !encode_codes_map(&ma64, codes_a, p.T, p.K, 64) || !encode_codes_map(&ma32, codes_a, p.T, p.K, 32) ||
         !encode_tiles_map(&msw, p.tiles_w, E * p.trows_w, p.ct, 1, kStepTiles<NV>) ||
         !encode_tiles_map(&msa, p.tiles_a, arows, p.ct, 2, kStepTiles<NV>))
         return RAZER_ERR_CUDA;
-    const int ntiles = (p.N + 255) / 256;
+    const int ntiles = (p.N + 255) / 256, step = pair_step(p, ntiles, pairs);
     const int64_t units = max_pieces(p.T, p.E, step) * ntiles;
     if (units > INT32_MAX - 1024) return RAZER_ERR_SHAPE;
     const int inject = fault_injection_enabled() ? 1 : 0;
     if (launch_pdl(mx_pair_kernel<NV, TOut, GATE>, 2u * (unsigned)std::min<int64_t>(units, pairs), (unsigned)kPairThreads, (size_t)Cfg::kSmem, st, mw,
-                   ma, msw, msa, p, ntiles, step, Y, inject) != cudaSuccess)
+                   ma, ma64, ma32, msw, msa, p, ntiles, step, Y, inject) != cudaSuccess)
         return RAZER_ERR_CUDA;
     return RAZER_OK;
 }
 
-static int64_t rows_per_group(int64_t T, int64_t E) { return E > 0 ? (T + E - 1) / E : T; }
-
 template <bool NV, typename TOut, bool GATE>
 static razer_status launch_mx(const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, TOut *Y, cudaStream_t st)
 {
-    if (rows_per_group(p.T, p.E) > 64) return launch_pair<NV, TOut, GATE>(codes_a, codes_w, p, kPairRows, Y, st);
+    if (rows_per_group(p.T, p.E) > 64) return launch_pair<NV, TOut, GATE>(codes_a, codes_w, p, Y, st);
     return launch_stream<NV, TOut, GATE, void>(nullptr, codes_a, codes_w, p, Y, st);
 }
 

@@ -141,7 +141,7 @@ def factor(ts_a, ts_w, e=0):
 
 SIZES = [(1, 128, 256), (8, 128, 64), (7, 40, 32), (16, 200, 96), (1, 1, 160), (33, 257, 512), (32, 128, 288), (65, 64, 1024), (64, 130, 480),
          (128, 128, 4128), (129, 300, 352), (300, 72, 640), (2, 512, 8192), (500, 600, 768),
-         (200, 256, 2048), (1500, 2600, 320), (700, 6000, 1088)]
+         (200, 256, 2048), (1500, 2600, 320), (700, 6000, 1088), (100, 64, 32), (193, 33, 64), (1, 5, 32)]
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
@@ -178,6 +178,61 @@ def test_product_gated(M, N, K, fmt):
         y = R.razer_gemm_mx(ca, sa, cw, sw, fmt, out, ts_a=ts_a, ts_w=ts_w, act="silu_mul")
         assert y.shape == (M, N // 2)
         ref.check(y, r, bound)
+
+
+@pytest.mark.parametrize("counts", [[70] * 40, [0] * 33 + [300] + [0] * 40 + [128, 1, 500, 90], [65, 192, 193, 64, 63]])
+def test_product_grouped_many_rows_a_group(counts):
+    # more groups than a warp looks up at once, empty ones between, pieces of every size
+    E, N, K, off = len(counts), 136, 160, offsets_of(counts, 2)
+    T = off[-1] + 3
+    ca, sa, a = packed(T, K, "mxfp4", T, offsets=off)
+    c, s = ref.random_packed(E * N, K, "mxfp4", E)
+    w = ref.values(c, s, "mxfp4").reshape(E, N, K)
+    sw = torch.stack([dev(ref.tile(x)) for x in s.reshape(E, N, -1)])
+    y = torch.full((T, N), 77.0, device=DEV)
+    R.razer_gemm_mx_grouped(ca, sa, torch.tensor(off, dtype=torch.int32, device=DEV), dev(c).view(E, N, K // 2), sw, out=y)
+    assert (y[:2] == 77).all() and (y[off[-1]:] == 77).all()
+    for e in np.flatnonzero(counts):
+        r, _, bound = ref.product(a[off[e]:off[e + 1]], w[e])
+        ref.check(y[off[e]:off[e + 1]], r, bound)
+
+
+@pytest.mark.parametrize("counts", [[150] + [0] * 19, [1, 0, 130, 0, 0, 3, 65, 2] + [0] * 12, [7] * 64])
+@pytest.mark.parametrize("gate", [False, True])
+def test_grouped_online_uneven_groups(counts, gate):
+    # few rows a group on average: quantized inside the product, groups of more than one piece among them
+    E, N, K, off = len(counts), 96, 544, offsets_of(counts, 1)
+    T = off[-1] + 2
+    x = dev(matrix(T, K, torch.bfloat16, T, 0.5))
+    c, s = ref.random_packed(E * N, K, "mxfp4", E, spread=2)
+    cw, sw = dev(c).view(E, N, K // 2), torch.stack([dev(ref.tile(v)) for v in s.reshape(E, N, -1)])
+    o = torch.tensor(off, dtype=torch.int32, device=DEV)
+    assert R.razer_gemm_mx_grouped_workspace_size(T, K, E) == 0
+    act = "silu_mul" if gate else None
+    codes, tiles = R.razer_quantize_mx(x, o)
+    y, z = (torch.full((T, N // 2 if gate else N), 77.0, device=DEV) for _ in range(2))
+    R.razer_gemm_mx_grouped(codes, tiles, o, cw, sw, act=act, out=y)
+    R.razer_gemm_mx_grouped_online(x, o, cw, sw, act=act, out=z)
+    assert torch.equal(y, z) and (z[0] == 77).all() and (z[off[-1]:] == 77).all()
+    a, w = ref.values(codes.cpu().numpy(), ref.untile(tiles.cpu().numpy(), T, K // 32, off), "mxfp4"), ref.values(c, s, "mxfp4").reshape(E, N, K)
+    for e in np.flatnonzero(counts):
+        r, _, bound = ref.product(a[off[e]:off[e + 1]], w[e])
+        if gate:
+            with np.errstate(over="ignore"):
+                r, bound = ref.silu_mul(r, bound)
+        ref.check(z[off[e]:off[e + 1]], r, bound)
+
+
+def test_online_nan_reaches_its_row_only():
+    for M in (5, 40):  # quantized inside the product, and before it
+        x = matrix(M, 256, torch.bfloat16, 1, 0.0)
+        x[2, 77] = float("nan")
+        x[3, 200] = float("inf")
+        cw, sw, _ = packed(130, 256, "mxfp4", 3)
+        y = R.razer_gemm_mx_online(dev(x), cw, sw, torch.float32)
+        bad = torch.zeros(M, dtype=torch.bool, device=DEV)
+        bad[2:4] = True
+        assert torch.isnan(y[bad]).all() and torch.isfinite(y[~bad]).all()
 
 
 def test_product_empty_shapes():
@@ -358,14 +413,18 @@ def test_offsets_that_break_the_rules_are_reported():
     assert R.razer_get_device_status() == 0
 
 
-def test_stalled_pipeline_reports_a_timeout_and_recovers():
-    M, N, K = 8, 128, 2048
+@pytest.mark.parametrize("M", [8, 300])
+def test_stalled_pipeline_reports_a_timeout_and_recovers(M):
+    N, K = 128, 2048
     ca, sa, a = packed(M, K, "mxfp4", 1)
     cw, sw, w = packed(N, K, "mxfp4", 2)
     prev = R.razer_debug_set_fault_injection(True)
     try:
         R.razer_gemm_mx(ca, sa, cw, sw)
         assert R.razer_get_device_status() == 7
+        if M <= 16:
+            R.razer_gemm_mx_online(dev(matrix(M, K, torch.bfloat16, 3, 0.0)), cw, sw)
+            assert R.razer_get_device_status() == 7
     finally:
         R.razer_debug_set_fault_injection(prev)
     y = R.razer_gemm_mx(ca, sa, cw, sw, out_dtype=torch.float32)
