@@ -236,6 +236,7 @@ struct RowWalk {
     {
         RowUnit u = {0, 0, 0, 0, 0};
         if (p.E == 0) {
+            if ((int64_t)t * step >= p.T) return u;  // 64 bits: T may be near 2^31
             u.row0 = t * step;
             u.count = min(step, p.T - u.row0);
             u.trow = u.row0 / kTileRows;
@@ -385,6 +386,10 @@ template <bool NV> struct StreamCfg {
     static_assert(kStreamRing / (kA + kStreamRows * 128 + 2 * kS) >= 3, "a ring for the widest unit");
 };
 static_assert(kStreamRows * 128 * 4 <= kStreamRing, "the sums of a cluster's CTA");
+// kFuseRows: up to so many rows a group, on average, an online call quantizes
+// in the product.  Two launches / one, us: 14336 x 4096, 8 rows 10.7 / 9.2, 16
+// rows 10.9 / 10.8, 24 rows 11.2 / 14.2; 28672 x 8192 24.8 / 24.2, 25.0 / 24.8,
+// 25.2 / 33.3: every CTA quantizes all of its rows again.
 
 template <bool NV, typename TOut, bool GATE, typename TIn>
 __global__ void __launch_bounds__(kStreamThreads, 2)
@@ -641,6 +646,11 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 // rows is what the FP4 rate asks for: an SM's operands per 256 k are (128 +
 // 96) x 128 bytes for 384 cycles of MMA, 75 bytes a cycle, where one CTA
 // alone would need 107.
+// Bound: a stage of 192 rows takes 401 cycles (MXFP4; NVFP4 415) against the
+// 384 of its MMAs, 390 (398) with the loads left out; of 64 rows 325, the
+// issuing warp's own latency.  4096 x 4096 x 4096 in 28.1 us (4.9 PFLOP/s).
+// Larger calls meet the power limit: 4096 x 14336 x 4096 takes 147,000 cycles,
+// 95 us, at 1.5 GHz.
 //   warps 0 and 14: bulk-tensor producers, a stage in turn (each CTA loads its
 //   own operands; the leader's barrier counts both); one warp alone needs 390
 //   cycles for a stage's four copies, as long as its MMAs take;
@@ -693,8 +703,8 @@ template <bool NV, typename TOut, bool GATE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a,
                    const __grid_constant__ CUtensorMap tmap_a64, const __grid_constant__ CUtensorMap tmap_a32,
-                   const __grid_constant__ CUtensorMap tmap_sw,
-                   const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ Problem p, int ntiles, int step, TOut *__restrict__ Y, int inject_stall)
+                   const __grid_constant__ CUtensorMap tmap_sw, const __grid_constant__ CUtensorMap tmap_sa,
+                   const __grid_constant__ Problem p, int ntiles, int step, TOut *__restrict__ Y, int inject_stall)
 {
     using Cfg = PairCfg<NV>;
     constexpr int STAGES = Cfg::kStages;
@@ -793,10 +803,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             // ---------------- MMA issuer (leader) ----------------
             const uint32_t lead = elect_one(), sfa = tmem + 2 * kPairRows, sfb = sfa + Cfg::kSfaCols;
             // One stage's copies, then its MMAs, the scales always in the same columns
-            // (copies and MMAs of one thread run in order).  The tensor pipe is the
-            // bound: 445 cycles a stage for MXFP4 with loads left out, 478 for NVFP4,
-            // 384 of them MMAs.  Copying the next stage's scales between the MMAs of
-            // this one, or two stages' at once, measured 10% slower.
+            // (copies and MMAs of one thread run in order).  Copying the next stage's
+            // scales between the MMAs of this one, or two stages' at once, measured
+            // 10% slower: the tensor pipe drains at each change between the two.
             uint32_t s = 0, ph = 0, ti = 0;
             bool ok = true, ready = false;
             RowWalk walk;
@@ -917,8 +926,8 @@ static int64_t max_pieces(int64_t T, int64_t E, int64_t step) { return E == 0 ? 
 
 // CTAs that share one unit along K: the power of two up to 8 that leaves the
 // busiest SM least to do (units * S CTAs, dealt out over the SMs, 1 / S of a
-// unit each; two stages at least; all of them resident), the smaller on a tie, since joining the sums
-// costs about 0.5 us.  MXFP4, packed, one row: 32 units of K = 4096 in 7.3 /
+// unit each; two stages at least; all of them resident), the smaller on a tie,
+// since joining the sums costs about 0.5 us.  MXFP4, packed, one row: 32 units of K = 4096 in 7.3 /
 // 6.3 / 5.8 / 6.5 us for S = 1 / 2 / 4 / 8; 112 units 9.2 / 9.2 / 13 / 21.
 static int stream_splits(int64_t units, int64_t steps)
 {
@@ -1041,10 +1050,13 @@ static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, 
     return RAZER_OK;
 }
 
+// The two kernels at up to 64 rows, us: 33 rows x 4096 x 4096 stream 8.1, pair
+// 8.6; 64 rows x 4096 x 14336 13.6 and 18.1, x 28672 x 4096 14.4 and 15.2; 128
+// rows 12.2 and 8.6, 19.5 and 18.0, 21.3 and 16.7.
 template <bool NV, typename TOut, bool GATE>
 static razer_status launch_mx(const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, TOut *Y, cudaStream_t st)
 {
-    if (rows_per_group(p.T, p.E) > 64) return launch_pair<NV, TOut, GATE>(codes_a, codes_w, p, Y, st);
+    if (rows_per_group(p.T, p.E) > kStreamRows) return launch_pair<NV, TOut, GATE>(codes_a, codes_w, p, Y, st);
     return launch_stream<NV, TOut, GATE, void>(nullptr, codes_a, codes_w, p, Y, st);
 }
 
@@ -1080,8 +1092,8 @@ bool gemm_mx_fuses(int64_t T, int64_t E) { return mx::rows_per_group(T, E) <= mx
 // scales.  X: the activations, to be quantized to MXFP4 inside the product
 // (gemm_mx_fuses), or NULL: they are packed.  The caller has checked every
 // argument; T, N > 0.
-razer_status run_gemm_mx(const void *X, razer_dtype x_dt, const uint8_t *codes_a, const uint8_t *tiles_a, const float *ts_a, int64_t T, const int32_t *offsets, int E,
-                         const uint8_t *codes_w, const uint8_t *tiles_w, const float *ts_w, razer_format fmt, int64_t N, int64_t K, int gate,
+razer_status run_gemm_mx(const void *X, razer_dtype x_dt, const uint8_t *codes_a, const uint8_t *tiles_a, const float *ts_a, int64_t T,
+                         const int32_t *offsets, int E, const uint8_t *codes_w, const uint8_t *tiles_w, const float *ts_w, razer_format fmt, int64_t N, int64_t K, int gate,
                          void *Y, razer_dtype out_dt, cudaStream_t st)
 {
     const bool nv = fmt == RAZER_FMT_NVFP4;

@@ -416,15 +416,23 @@ _U8 = torch.uint8
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _mx_call(fn: str, call, dev, stream, *args):
-    """Calls the library with dev current and, without a stream, on dev's current stream."""
+def _mx_call(fn: str, call, dev, *args):
+    """Calls the library with dev current, on dev's current stream."""
     index = dev.index
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            return _mx_call(fn, call, dev, stream, *args)
-    st = call(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+            return _mx_call(fn, call, dev, *args)
+    st = call(*args, _raw_stream(index))
     if st:
         raise RazerError(fn, st)
+
+
+def _mx_on(fn: str, stream, dev, call):
+    """call() with stream current: what it allocates then belongs to that stream."""
+    if stream.device != dev:
+        raise ValueError(f"{fn}: a stream of {stream.device} for tensors on {dev}")
+    with torch.cuda.stream(stream):
+        return call()
 
 
 def _mx_ptr(t):
@@ -467,13 +475,15 @@ def razer_quantize_mx(X: torch.Tensor, offsets: torch.Tensor | None = None, *, c
     (codes [M, K/2] u8, scale tiles u8).  offsets (int32 [E + 1], device): rows
     in E groups, as razer_gemm_mx_grouped takes them; rows of no group are left out."""
     fn = "razer_quantize_mx"
+    if stream is not None:
+        return _mx_on(fn, stream, X.device, lambda: razer_quantize_mx(X, offsets, codes=codes, scales=scales))
     M, K = _mx_matrix(fn, "X", X)
     dev = X.device
     E = 0 if offsets is None else _mx_groups(fn, offsets, dev)
     r, c, b = shape = _mx_tiles(M, K, 32, E)
     codes = torch.empty(M, K // 2, dtype=_U8, device=dev) if codes is None else _mx_shape(fn, "codes", codes, (M, K // 2), _U8, dev)
     scales = torch.empty(r, c, b, dtype=_U8, device=dev) if scales is None else _mx_shape(fn, "scales", scales, shape, _U8, dev)
-    _mx_call(fn, load().razer_quantize_mx, dev, stream, X.data_ptr(), _DT.get(X.dtype, -1), M, K, _mx_ptr(offsets), E, codes.data_ptr(),
+    _mx_call(fn, load().razer_quantize_mx, dev, X.data_ptr(), _DT.get(X.dtype, -1), M, K, _mx_ptr(offsets), E, codes.data_ptr(),
              scales.data_ptr())
     return codes, scales
 
@@ -482,13 +492,15 @@ def razer_dequant_mx(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torch.
                      out=None, stream=None):
     """Decode MXFP4 codes [M, K/2] with their scale tiles to [M, K] (one rounding to out_dtype)."""
     fn = "razer_dequant_mx"
+    if stream is not None:
+        return _mx_on(fn, stream, codes.device, lambda: razer_dequant_mx(codes, scales, out_dtype, offsets, out=out))
     M, K2 = shape = _mx_matrix(fn, "codes", codes)
     dev, K = codes.device, 2 * K2
     E = 0 if offsets is None else _mx_groups(fn, offsets, dev)
     _mx_shape(fn, "codes", codes, shape, _U8, dev)
     _mx_shape(fn, "scales", scales, _mx_tiles(M, K, 32, E), _U8, dev)
     out = torch.empty(M, K, dtype=out_dtype, device=dev) if out is None else _mx_shape(fn, "out", out, (M, K), out.dtype, dev)
-    _mx_call(fn, load().razer_dequant_mx, dev, stream, codes.data_ptr(), scales.data_ptr(), M, K, _mx_ptr(offsets), E, out.data_ptr(),
+    _mx_call(fn, load().razer_dequant_mx, dev, codes.data_ptr(), scales.data_ptr(), M, K, _mx_ptr(offsets), E, out.data_ptr(),
              _DT.get(out.dtype, -1))
     return out
 
@@ -497,6 +509,8 @@ def razer_tile_scales(scales: torch.Tensor, offsets: torch.Tensor | None = None,
     """Row-major scale bytes [R, C] or [B, R, C] (as the NVFP4 quantizers write
     them) to scale tiles [..., tile rows, ceil(C/4), 512]; offsets: R rows in groups."""
     fn = "razer_tile_scales"
+    if stream is not None:
+        return _mx_on(fn, stream, scales.device, lambda: razer_tile_scales(scales, offsets, out=out))
     if scales.dim() == 3 and offsets is not None:
         raise ValueError(f"{fn}: row groups need [R, C] scales")
     shape = _mx_matrix(fn, "scales", scales, 3 if scales.dim() == 3 else 2)
@@ -506,7 +520,7 @@ def razer_tile_scales(scales: torch.Tensor, offsets: torch.Tensor | None = None,
     R, C = shape[-2:]
     tiles = (*shape[:-2], R // 128 + E if E else -(-R // 128), -(-C // 4), 512)
     out = torch.empty(*tiles, dtype=torch.uint8, device=dev) if out is None else _mx_shape(fn, "out", out, tiles, torch.uint8, dev)
-    _mx_call(fn, load().razer_tile_scales, dev, stream, scales.data_ptr(), shape[0] if len(shape) == 3 else 1, R, C, _mx_ptr(offsets), E,
+    _mx_call(fn, load().razer_tile_scales, dev, scales.data_ptr(), shape[0] if len(shape) == 3 else 1, R, C, _mx_ptr(offsets), E,
              out.data_ptr())
     return out
 
@@ -539,6 +553,9 @@ def _mx_out(fn: str, out, rows: int, N: int, act: int, out_dtype, dev, groups: i
 
 
 def _mx_product(fn, call, codes_a, scales_a, offsets, codes_w, scales_w, fmt, out_dtype, ts_a, ts_w, act, out, stream):
+    if stream is not None:
+        return _mx_on(fn, stream, codes_a.device, lambda: _mx_product(fn, call, codes_a, scales_a, offsets, codes_w, scales_w, fmt, out_dtype,
+                                                                      ts_a, ts_w, act, out, None))
     T, K2 = shape = _mx_matrix(fn, "codes_a", codes_a)
     dev, K = codes_a.device, 2 * K2
     E, f, a = _mx_groups(fn, offsets, dev), _fmt(fmt), _mx_act(fn, act)
@@ -550,7 +567,7 @@ def _mx_product(fn, call, codes_a, scales_a, offsets, codes_w, scales_w, fmt, ou
     N = _mx_weights(fn, codes_w, scales_w, E, K, block, dev, ts_w)
     out = _mx_out(fn, out, T, N, a, out_dtype, dev, E)
     groups = (offsets.data_ptr(), E) if E else ()
-    _mx_call(fn, call, dev, stream, codes_a.data_ptr(), scales_a.data_ptr(), _mx_ptr(ts_a), T, *groups, codes_w.data_ptr(), scales_w.data_ptr(),
+    _mx_call(fn, call, dev, codes_a.data_ptr(), scales_a.data_ptr(), _mx_ptr(ts_a), T, *groups, codes_w.data_ptr(), scales_w.data_ptr(),
              _mx_ptr(ts_w), f, N, K, a, out.data_ptr(), _DT.get(out.dtype, -1))
     return out
 
@@ -583,6 +600,8 @@ def razer_gemm_mx_grouped_workspace_size(T: int, K: int, groups: int) -> int:
 
 
 def _mx_online(fn, call, X, offsets, codes_w, scales_w, out_dtype, act, out, workspace, stream):
+    if stream is not None:
+        return _mx_on(fn, stream, X.device, lambda: _mx_online(fn, call, X, offsets, codes_w, scales_w, out_dtype, act, out, workspace, None))
     T, K = _mx_matrix(fn, "X", X)
     dev = X.device
     E = 0 if offsets is None else _mx_groups(fn, offsets, dev)
@@ -599,7 +618,7 @@ def _mx_online(fn, call, X, offsets, codes_w, scales_w, out_dtype, act, out, wor
     else:
         ws, wp = workspace.numel() * workspace.element_size(), workspace.data_ptr()
     groups = (offsets.data_ptr(), E) if E else ()
-    _mx_call(fn, call, dev, stream, X.data_ptr(), _DT.get(X.dtype, -1), T, *groups, codes_w.data_ptr(), scales_w.data_ptr(), N, K, a,
+    _mx_call(fn, call, dev, X.data_ptr(), _DT.get(X.dtype, -1), T, *groups, codes_w.data_ptr(), scales_w.data_ptr(), N, K, a,
              out.data_ptr(), _DT.get(out.dtype, -1), wp, ws)
     return out
 

@@ -431,3 +431,35 @@ def test_stalled_pipeline_reports_a_timeout_and_recovers(M):
     r, _, bound = ref.product(a, w)
     ref.check(y, r, bound)
     assert R.razer_get_device_status() == 0
+
+
+def test_stream_argument_owns_what_it_allocates():
+    # the workspace of an online call on another stream must not be handed to
+    # work of the current one before that stream is done with it
+    M, N, K = 200, 4096, 4096
+    cw, sw, _ = packed(N, K, "mxfp4", 1)
+    x = dev(matrix(M, K, torch.bfloat16, 2, 0.0))
+    want = R.razer_gemm_mx_online(x, cw, sw)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        y = R.razer_gemm_mx_online(x, cw, sw, stream=side)
+        junk = torch.full((R.razer_workspace_size(R.RAZER_OP_GEMM_MX_ONLINE, M, N, K),), 255, dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        del junk, y
+
+
+def test_first_call_of_a_size_in_a_capture():
+    # nothing a call does for the first time (attributes, occupancy) is barred while capturing
+    M, N, K = 130, 258, 96
+    ca, sa, a = packed(M, K, "nvfp4", 1)
+    cw, sw, w = packed(N, K, "nvfp4", 2)
+    one, y = torch.ones(1, device=DEV), torch.zeros(M, N // 2, dtype=torch.float16, device=DEV)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        R.razer_gemm_mx(ca, sa, cw, sw, "nvfp4", ts_a=one, ts_w=one, act="silu_mul", out=y)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, R.razer_gemm_mx(ca, sa, cw, sw, "nvfp4", torch.float16, ts_a=one, ts_w=one, act="silu_mul"))

@@ -1,0 +1,53 @@
+"""The microscaled 4-bit operators past 2^31: codes of more than 2^31 bytes,
+outputs of more than 2^31 elements, checked on sampled rows."""
+import numpy as np
+import pytest
+import torch
+
+import bit_quantization_razer_b200 as R
+from tests import mx_reference as ref
+from tests.gpu_helpers import cuda
+
+pytestmark = [pytest.mark.gpu, cuda]
+DEV = "cuda:0"
+
+
+def test_quantize_and_product_past_2_31():
+    M, N, K = 540_003, 4096, 8192
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(11)
+    x = torch.empty(M, K, dtype=torch.bfloat16, device=DEV).normal_(0.0, 1.0, generator=g)
+    w = torch.empty(N, K, dtype=torch.bfloat16, device=DEV).normal_(0.0, 0.02, generator=g)
+    codes, scales = R.razer_quantize_mx(x)
+    assert codes.numel() > 1 << 31
+    rows = np.unique(np.concatenate([[0, M - 1, (1 << 31) * 2 // K, (1 << 31) * 2 // K + 1, (1 << 31) // N, (1 << 31) // N + 1],
+                                     np.random.default_rng(0).integers(0, M, 26)]))
+    at = torch.from_numpy(rows).to(DEV)
+    rc, rs = ref.quantize(x[at].double().cpu().numpy())
+    assert np.array_equal(ref.unpack(codes[at].cpu().numpy()), rc)
+    c = torch.arange(K // 32, device=DEV)
+    got = scales[at[:, None] // 128, c[None] // 4, ((at % 32) * 16 + at % 128 // 32 * 4)[:, None] + c[None] % 4]
+    assert np.array_equal(got.cpu().numpy(), rs)
+    back = R.razer_dequant_mx(codes, scales, torch.bfloat16)  # exact in bf16
+    a = ref.values(codes[at].cpu().numpy(), rs, "mxfp4")
+    assert np.array_equal(back[at].double().cpu().numpy(), a)
+    del x, back
+    cw, sw = R.razer_quantize_mx(w)
+    wv = ref.values(cw.cpu().numpy(), ref.untile(sw.cpu().numpy(), N, K // 32), "mxfp4")
+    y = R.razer_gemm_mx(codes, scales, cw, sw)
+    assert y.numel() > 1 << 31
+    r, _, bound = ref.product(a, wv)
+    ref.check(y[at], r, bound)
+    # the same rows as two groups that meet near the end
+    off = [3, M - 130, M - 1]
+    o = torch.tensor(off, dtype=torch.int32, device=DEV)
+    tiles = torch.zeros(R.razer_scale_tiles_shape(M, K, "mxfp4", 2), dtype=torch.uint8, device=DEV)
+    flat = scales.view(-1, scales.shape[1], 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(-1, scales.shape[1] * 4)[:M, :K // 32].contiguous()
+    R.razer_tile_scales(flat, o, out=tiles)
+    y2 = torch.zeros_like(y)
+    R.razer_gemm_mx_grouped(codes, tiles, o, torch.stack([cw, cw]), torch.stack([sw, sw]), out=y2)
+    inside = torch.from_numpy(rows[(rows >= 3) & (rows < M - 1)]).to(DEV)
+    assert torch.equal(y2[inside], y[inside]) and not y2[:3].any() and not y2[M - 1].any()
+    assert torch.equal(y2[M - 200:M - 1], y[M - 200:M - 1])
