@@ -171,13 +171,20 @@ __device__ __forceinline__ void issue_mmas(uint32_t lead, uint32_t acc, uint32_t
 
 // silu(g) * u = g / (1 + exp(-g)) * u.  16-bit outputs take the hardware's
 // 2^x and reciprocal: the exponent's rounding, |g| log2(e) 2^-24, bounds the
-// relative error by 6e-6 where the result is not yet 0 (|g| < 88), against the
-// 2^-9 (2^-12) of the output's own rounding; with expf and an IEEE division
-// the epilogue of 512 x 28672 x 4096 took longer than its MMAs.
+// relative error by 6e-6 where the result is not yet 0 (|g| < 87; below, 2^x
+// passes the range and the reciprocal is 0), against the 2^-9 (2^-12) of the
+// output's own rounding; with expf and an IEEE division the epilogue of 512 x
+// 28672 x 4096 took longer than its MMAs.
 template <typename TOut> __device__ __forceinline__ float silu_mul(float g, float u)
 {
-    if constexpr (sizeof(TOut) == 2) return __fdividef(g, 1.0f + __expf(-g)) * u;
-    else return g / (1.0f + expf(-g)) * u;
+    if constexpr (sizeof(TOut) == 2) {
+        float e, r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+        return g * r * u;
+    } else {
+        return g / (1.0f + expf(-g)) * u;
+    }
 }
 
 // One product: N, K of the weights, T activation rows (in all groups), E = 0:
@@ -271,18 +278,38 @@ template <typename TOut> __device__ __forceinline__ void store_pair(TOut *p, flo
 // the rows row .. row + count - 1 (at most 32).  Adjacent lanes swap halves of
 // two columns, so that the even lane finishes the first row and the odd lane
 // the second: a gated pair meets in one lane and every lane computes one, and
-// 16-bit outputs leave in pairs, 16 stores instead of 32.  ALL: 32 rows; the
-// 16 chains are then free of branches and run into each other (with a test
-// between them a unit of 192 rows took 7,000 cycles, longer than its 16 stages
-// of MMAs; with one store per column and lane and the gate tested inside the
-// loop 15,700).
-template <typename TOut, bool GATE, bool ALL>
-__device__ __forceinline__ void write_columns_n(const float (&v)[32], float scale, TOut *__restrict__ Y, int64_t ldy, int count, bool mine, int lane)
+// 16-bit outputs leave in pairs, 16 stores instead of 32; gated ones swap once
+// more between lanes two apart, 8 stores.  ALL: 32 rows; the chains are then
+// free of branches and run into each other (with a test between them a unit of
+// 192 rows took 7,000 cycles, longer than its 16 stages of MMAs; with one store
+// per column and lane and the gate tested inside the loop 15,700; now 3,500,
+// gated 4,700).  PAIRS: rows of an even length, so that pairs are 4-byte
+// aligned.
+template <typename TOut, bool GATE, bool ALL, bool PAIRS>
+__device__ __forceinline__ void write_columns_n(const float (&v)[32], float scale, TOut *__restrict__ Y, int64_t ldy, int count, bool mine, int n,
+                                                int lane)
 {
-    const int odd = lane & 1;
-    if constexpr (GATE || sizeof(TOut) == 2) {
+    const int odd = lane & 1, high = (lane >> 1) & 1;
+    if constexpr (sizeof(TOut) == 2 && GATE && PAIRS) {
+        // four rows a step; outputs n / 2 & ~1 and n / 2 | 1
+        TOut *y = Y + (odd + 2 * high) * ldy + (n / 2 & ~1);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            if (!ALL && i >= count) break;
+            float r[2];
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const float keep = (odd ? v[i + 2 * j + 1] : v[i + 2 * j]) * scale, give = (odd ? v[i + 2 * j] : v[i + 2 * j + 1]) * scale;
+                const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+                r[j] = silu_mul<TOut>(odd ? got : keep, odd ? keep : got);  // row 2j of the weights gates row 2j + 1
+            }
+            const float got = __shfl_xor_sync(0xffffffffu, high ? r[0] : r[1], 2);
+            if (mine && (ALL || i + odd + 2 * high < count)) store_pair<TOut>(y, high ? got : r[0], high ? r[1] : got);
+            y += 4 * ldy;
+        }
+    } else if constexpr (GATE || (sizeof(TOut) == 2 && PAIRS)) {
         // two rows a step
-        TOut *y = Y + (odd ? ldy : 0);
+        TOut *y = Y + odd * ldy + (GATE ? n / 2 : n & ~1);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
             if (!ALL && i >= count) break;
@@ -290,13 +317,13 @@ __device__ __forceinline__ void write_columns_n(const float (&v)[32], float scal
             const float got = __shfl_xor_sync(0xffffffffu, give, 1);
             const float even = odd ? got : keep, next = odd ? keep : got;  // columns n & ~1 and n | 1
             if (mine && (ALL || i + odd < count)) {
-                if constexpr (GATE) store1<TOut>(y, silu_mul<TOut>(even, next));  // row 2j of the weights gates row 2j + 1
+                if constexpr (GATE) store1<TOut>(y, silu_mul<TOut>(even, next));
                 else store_pair<TOut>(y, even, next);
             }
             y += 2 * ldy;
         }
     } else {
-        TOut *y = Y;
+        TOut *y = Y + n;
 #pragma unroll
         for (int i = 0; i < 32; i++) {
             if (!ALL && i >= count) break;
@@ -311,20 +338,13 @@ __device__ __forceinline__ void write_columns(const float (&v)[32], float scale,
 {
     const bool mine = n < N;
     TOut *y = Y + (int64_t)row * ldy;
-    if constexpr (!GATE && sizeof(TOut) == 2) {
-        if (ldy & 1) {  // rows of an odd length: no pairs
-            y += n;
-#pragma unroll
-            for (int i = 0; i < 32; i++) {
-                if (mine && i < count) store1<TOut>(y, v[i] * scale);
-                y += ldy;
-            }
-            return;
-        }
+    if (sizeof(TOut) == 2 && (ldy & 1) == 0) {
+        if (count >= 32) write_columns_n<TOut, GATE, true, true>(v, scale, y, ldy, count, mine, n, lane);
+        else write_columns_n<TOut, GATE, false, true>(v, scale, y, ldy, count, mine, n, lane);
+    } else {
+        if (count >= 32) write_columns_n<TOut, GATE, true, false>(v, scale, y, ldy, count, mine, n, lane);
+        else write_columns_n<TOut, GATE, false, false>(v, scale, y, ldy, count, mine, n, lane);
     }
-    y += GATE ? n / 2 : (sizeof(TOut) == 2 ? n & ~1 : n);
-    if (count >= 32) write_columns_n<TOut, GATE, true>(v, scale, y, ldy, count, mine, lane);
-    else write_columns_n<TOut, GATE, false>(v, scale, y, ldy, count, mine, lane);
 }
 
 // shared-memory address of the same object in CTA `rank` of the cluster
