@@ -557,6 +557,8 @@ razer_status razer_gemm_mx_grouped(const uint8_t *codes_a, const uint8_t *scales
  *              aligned; contents on entry ignored): the packed activations.  0
  *              bytes (NULL) for up to 16 rows, or 16 per group on average: the
  *              product's kernel then quantizes them itself, in one launch.
+ *              Calls that may overlap on the GPU (two streams, two graphs)
+ *              need a workspace each.
  */
 razer_status razer_gemm_mx_online(const void *X, razer_dtype x_dt, int64_t M, const uint8_t *codes_w,
                                   const uint8_t *scales_w, int64_t N, int64_t K, razer_act act, void *Y,

@@ -163,3 +163,17 @@ def test_python_calls_refuse_what_the_library_cannot_see():
                  lambda: R.razer_gemm_mx_grouped_online(x, None, u8, t), lambda: R.razer_tile_scales(u8.view(1, 4, 32), torch.zeros(2))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_plain_c_consumer(lib, tmp_path):
+    # the header's microscaled calls from a C program, every warning an error
+    import os
+    import subprocess
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    libdir, exe = os.path.join(root, "bit_quantization_razer_b200"), str(tmp_path / "mx_abi_consumer")
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(root, "include"),
+                    os.path.join(root, "tests", "mx_abi_consumer.c"), "-L", libdir, "-lrazer", "-Wl,-rpath," + libdir, "-o", exe], check=True)
+    out = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert out.returncode == 0, out.stderr
+    assert "all checks passed" in out.stdout
