@@ -399,75 +399,67 @@ def razer_gemm(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, ts: t
 # Scale tiles are uint8 tensors [..., tile rows, tile columns, 512]; include/razer.h
 # gives their layout and that of row groups.
 
-def _mx_bad(fn: str, name: str, t, shape, dtype, dev):
-    got = "None" if t is None else f"{tuple(t.shape)} {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}"
-    raise ValueError(f"{fn}: {name} must be a contiguous {tuple(shape)} {dtype} tensor on {dev}, got {got}")
-
-
-def _mx_shape(fn: str, name: str, t, shape, dtype, dev):
-    """t is a contiguous tensor of this shape, type and device (the library sees only its address)."""
-    if t is None or t.shape != shape or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
-        _mx_bad(fn, name, t, shape, dtype, dev)
-    return t
-
-
-_U8 = torch.uint8
+_U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
 # torch.cuda.current_stream() builds an object, 3 us: as much as a launch
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _mx_call(fn: str, call, dev, *args):
+def _mx_bad(fn: str, name: str, t, shape, dtype, dev: int):
+    got = "None" if t is None else f"{tuple(t.shape)} {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}"
+    raise ValueError(f"{fn}: {name} must be a contiguous {tuple(shape)} {dtype or ''} tensor on cuda:{max(dev, 0)}, got {got}")
+
+
+def _mx_ptr(fn: str, name: str, t, shape, dtype, dev: int) -> int:
+    """Address of t, a contiguous tensor of this shape, type and device (the library sees only the address)."""
+    if t is None or t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _mx_bad(fn, name, t, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _mx_first(fn: str, name: str, x, dims: int):
+    """(shape, device index) of the tensor that sets a call's device: contiguous, of so many dimensions, on a GPU."""
+    shape, dev = x.shape, x.get_device()
+    if len(shape) != dims or dev < 0 or not x.is_contiguous():
+        _mx_bad(fn, name, x, (f"{dims}-dimensional",), None, dev)
+    return shape, dev
+
+
+def _mx_call(fn: str, call, dev: int, *args):
     """Calls the library with dev current, on dev's current stream."""
-    index = dev.index
-    if index != torch._C._cuda_getDevice():
+    if dev != _current_device():
         with torch.cuda.device(dev):
             return _mx_call(fn, call, dev, *args)
-    st = call(*args, _raw_stream(index))
+    st = call(*args, _raw_stream(dev))
     if st:
         raise RazerError(fn, st)
 
 
-def _mx_on(fn: str, stream, dev, call):
+def _mx_on(fn: str, stream, t, call):
     """call() with stream current: what it allocates then belongs to that stream."""
-    if stream.device != dev:
-        raise ValueError(f"{fn}: a stream of {stream.device} for tensors on {dev}")
+    if stream.device != t.device:
+        raise ValueError(f"{fn}: a stream of {stream.device} for tensors on {t.device}")
     with torch.cuda.stream(stream):
         return call()
 
 
-def _mx_ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _mx_matrix(fn: str, name: str, x, dims: int = 2):
-    shape = x.shape
-    if len(shape) != dims or not x.is_cuda or not x.is_contiguous():
-        raise ValueError(f"{fn}: {name} must be a contiguous {dims}-dimensional CUDA tensor, got {tuple(x.shape)} on {x.device}"
-                         f"{'' if x.is_contiguous() else ', not contiguous'}")
-    return shape
-
-
-def _mx_groups(fn: str, offsets, dev) -> int:
-    """Number of row groups (0: none given)."""
-    if offsets is None:
-        return 0
-    if offsets.dim() != 1 or offsets.shape[0] < 2:
+def _mx_groups(fn: str, offsets, dev: int) -> tuple[int, int]:
+    """(address of the offsets, number of row groups)."""
+    shape = offsets.shape
+    if len(shape) != 1 or shape[0] < 2:
         raise ValueError(f"{fn}: offsets must hold one entry more than there are groups, and a group at least")
-    _mx_shape(fn, "offsets", offsets, offsets.shape, torch.int32, dev)
-    return offsets.shape[0] - 1
+    return _mx_ptr(fn, "offsets", offsets, shape, _I32, dev), shape[0] - 1
 
 
-def _mx_tiles(R: int, K: int, block: int, groups: int = 0) -> tuple[int, int, int]:
-    return (R // 128 + groups if groups else -(-R // 128), -(-K // (4 * block)), 512)
-
-
-def _mx_block(fmt) -> int:
-    return 16 if _fmt(fmt) == RAZER_FMT_NVFP4 else 32
+def _mx_format(fn: str, fmt) -> tuple[int, int]:
+    """(format, elements per block) of a format that has scale tiles; others are left to the library."""
+    f = FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
+    return f, 16 if f == RAZER_FMT_NVFP4 else 32
 
 
 def razer_scale_tiles_shape(R: int, K: int, fmt="mxfp4", groups: int = 0) -> tuple[int, int, int]:
     """Shape of the scale tiles of [R, K] codes, or of R rows in `groups` row groups."""
-    return _mx_tiles(R, K, _mx_block(fmt), groups)
+    per = 4 * _mx_format("razer_scale_tiles_shape", fmt)[1]
+    return (R // 128 + groups if groups else (R + 127) // 128, (K + per - 1) // per, 512)
 
 
 def razer_quantize_mx(X: torch.Tensor, offsets: torch.Tensor | None = None, *, codes=None, scales=None, stream=None):
@@ -476,15 +468,21 @@ def razer_quantize_mx(X: torch.Tensor, offsets: torch.Tensor | None = None, *, c
     in E groups, as razer_gemm_mx_grouped takes them; rows of no group are left out."""
     fn = "razer_quantize_mx"
     if stream is not None:
-        return _mx_on(fn, stream, X.device, lambda: razer_quantize_mx(X, offsets, codes=codes, scales=scales))
-    M, K = _mx_matrix(fn, "X", X)
-    dev = X.device
-    E = 0 if offsets is None else _mx_groups(fn, offsets, dev)
-    r, c, b = shape = _mx_tiles(M, K, 32, E)
-    codes = torch.empty(M, K // 2, dtype=_U8, device=dev) if codes is None else _mx_shape(fn, "codes", codes, (M, K // 2), _U8, dev)
-    scales = torch.empty(r, c, b, dtype=_U8, device=dev) if scales is None else _mx_shape(fn, "scales", scales, shape, _U8, dev)
-    _mx_call(fn, load().razer_quantize_mx, dev, X.data_ptr(), _DT.get(X.dtype, -1), M, K, _mx_ptr(offsets), E, codes.data_ptr(),
-             scales.data_ptr())
+        return _mx_on(fn, stream, X, lambda: razer_quantize_mx(X, offsets, codes=codes, scales=scales))
+    (M, K), dev = _mx_first(fn, "X", X, 2)
+    op, E = (None, 0) if offsets is None else _mx_groups(fn, offsets, dev)
+    rows, cols = M // 128 + E if E else (M + 127) // 128, (K + 127) // 128
+    if codes is None:
+        codes = torch.empty(M, K // 2, dtype=_U8, device=X.device)
+        cp = codes.data_ptr()
+    else:
+        cp = _mx_ptr(fn, "codes", codes, (M, K // 2), _U8, dev)
+    if scales is None:
+        scales = torch.empty(rows, cols, 512, dtype=_U8, device=X.device)
+        sp = scales.data_ptr()
+    else:
+        sp = _mx_ptr(fn, "scales", scales, (rows, cols, 512), _U8, dev)
+    _mx_call(fn, load().razer_quantize_mx, dev, X.data_ptr(), _DT.get(X.dtype, -1), M, K, op, E, cp, sp)
     return codes, scales
 
 
@@ -493,15 +491,17 @@ def razer_dequant_mx(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torch.
     """Decode MXFP4 codes [M, K/2] with their scale tiles to [M, K] (one rounding to out_dtype)."""
     fn = "razer_dequant_mx"
     if stream is not None:
-        return _mx_on(fn, stream, codes.device, lambda: razer_dequant_mx(codes, scales, out_dtype, offsets, out=out))
-    M, K2 = shape = _mx_matrix(fn, "codes", codes)
-    dev, K = codes.device, 2 * K2
-    E = 0 if offsets is None else _mx_groups(fn, offsets, dev)
-    _mx_shape(fn, "codes", codes, shape, _U8, dev)
-    _mx_shape(fn, "scales", scales, _mx_tiles(M, K, 32, E), _U8, dev)
-    out = torch.empty(M, K, dtype=out_dtype, device=dev) if out is None else _mx_shape(fn, "out", out, (M, K), out.dtype, dev)
-    _mx_call(fn, load().razer_dequant_mx, dev, codes.data_ptr(), scales.data_ptr(), M, K, _mx_ptr(offsets), E, out.data_ptr(),
-             _DT.get(out.dtype, -1))
+        return _mx_on(fn, stream, codes, lambda: razer_dequant_mx(codes, scales, out_dtype, offsets, out=out))
+    (M, K2), dev = _mx_first(fn, "codes", codes, 2)
+    if codes.dtype is not _U8:
+        _mx_bad(fn, "codes", codes, codes.shape, _U8, dev)
+    op, E = (None, 0) if offsets is None else _mx_groups(fn, offsets, dev)
+    sp = _mx_ptr(fn, "scales", scales, (M // 128 + E if E else (M + 127) // 128, (K2 + 63) // 64, 512), _U8, dev)
+    if out is None:
+        out = torch.empty(M, 2 * K2, dtype=out_dtype, device=codes.device)
+    else:
+        _mx_ptr(fn, "out", out, (M, 2 * K2), out.dtype, dev)
+    _mx_call(fn, load().razer_dequant_mx, dev, codes.data_ptr(), sp, M, 2 * K2, op, E, out.data_ptr(), _DT.get(out.dtype, -1))
     return out
 
 
@@ -510,18 +510,22 @@ def razer_tile_scales(scales: torch.Tensor, offsets: torch.Tensor | None = None,
     them) to scale tiles [..., tile rows, ceil(C/4), 512]; offsets: R rows in groups."""
     fn = "razer_tile_scales"
     if stream is not None:
-        return _mx_on(fn, stream, scales.device, lambda: razer_tile_scales(scales, offsets, out=out))
-    if scales.dim() == 3 and offsets is not None:
-        raise ValueError(f"{fn}: row groups need [R, C] scales")
-    shape = _mx_matrix(fn, "scales", scales, 3 if scales.dim() == 3 else 2)
-    dev = scales.device
-    _mx_shape(fn, "scales", scales, shape, torch.uint8, dev)
-    E = _mx_groups(fn, offsets, dev)
+        return _mx_on(fn, stream, scales, lambda: razer_tile_scales(scales, offsets, out=out))
+    dims = 2 if offsets is not None or len(scales.shape) != 3 else 3
+    shape, dev = _mx_first(fn, "scales", scales, dims)
+    if scales.dtype is not _U8:
+        _mx_bad(fn, "scales", scales, shape, _U8, dev)
+    op, E = (None, 0) if offsets is None else _mx_groups(fn, offsets, dev)
     R, C = shape[-2:]
-    tiles = (*shape[:-2], R // 128 + E if E else -(-R // 128), -(-C // 4), 512)
-    out = torch.empty(*tiles, dtype=torch.uint8, device=dev) if out is None else _mx_shape(fn, "out", out, tiles, torch.uint8, dev)
-    _mx_call(fn, load().razer_tile_scales, dev, scales.data_ptr(), shape[0] if len(shape) == 3 else 1, R, C, _mx_ptr(offsets), E,
-             out.data_ptr())
+    tiles = (R // 128 + E if E else (R + 127) // 128, (C + 3) // 4, 512)
+    if dims == 3:
+        tiles = (shape[0], *tiles)
+    if out is None:
+        out = torch.empty(*tiles, dtype=_U8, device=scales.device)
+        to = out.data_ptr()
+    else:
+        to = _mx_ptr(fn, "out", out, tiles, _U8, dev)
+    _mx_call(fn, load().razer_tile_scales, dev, scales.data_ptr(), shape[0] if dims == 3 else 1, R, C, op, E, to)
     return out
 
 
@@ -531,44 +535,42 @@ def _mx_act(fn: str, act) -> int:
     return ACTS[act]
 
 
-def _mx_weights(fn: str, codes_w, scales_w, E: int, K: int, block: int, dev, ts_w=None) -> int:
-    """Checks packed weights [N, K/2], or [E, N, K/2] for row groups; returns N."""
+def _mx_weights(fn: str, codes_w, scales_w, E: int, K2: int, block: int, dev: int):
+    """Checks packed weights [N, K/2], or [E, N, K/2] for row groups; returns N and their addresses."""
     shape = codes_w.shape
-    if len(shape) != (3 if E else 2) or shape[-1] != K // 2 or (E and shape[0] != E):
-        raise ValueError(f"{fn}: codes_w must be {f'[{E}, N, {K // 2}]' if E else f'[N, {K // 2}]'}, got {tuple(shape)}")
+    if len(shape) != (3 if E else 2) or shape[-1] != K2 or (E and shape[0] != E):
+        raise ValueError(f"{fn}: codes_w must be {f'[{E}, N, {K2}]' if E else f'[N, {K2}]'}, got {tuple(shape)}")
     N = shape[-2]
-    _mx_shape(fn, "codes_w", codes_w, shape, _U8, dev)
-    tiles = (-(-N // 128), -(-K // (4 * block)), 512)
-    _mx_shape(fn, "scales_w", scales_w, (E, *tiles) if E else tiles, _U8, dev)
-    if ts_w is not None:
-        _mx_shape(fn, "ts_w", ts_w, (E or 1,), torch.float32, dev)
-    return N
+    tiles = ((N + 127) // 128, (2 * K2 + 4 * block - 1) // (4 * block), 512)
+    return N, _mx_ptr(fn, "codes_w", codes_w, shape, _U8, dev), _mx_ptr(fn, "scales_w", scales_w, (E, *tiles) if E else tiles, _U8, dev)
 
 
-def _mx_out(fn: str, out, rows: int, N: int, act: int, out_dtype, dev, groups: int):
-    cols = N // 2 if act else N
+def _mx_out(fn: str, out, rows: int, cols: int, out_dtype, like, E: int, dev: int):
     if out is None:  # rows of no group are not written
-        return (torch.zeros if groups else torch.empty)(rows, cols, dtype=out_dtype, device=dev)
-    return _mx_shape(fn, "out", out, (rows, cols), out.dtype, dev)
+        return (torch.zeros if E else torch.empty)(rows, cols, dtype=out_dtype, device=like.device)
+    _mx_ptr(fn, "out", out, (rows, cols), out.dtype, dev)
+    return out
 
 
 def _mx_product(fn, call, codes_a, scales_a, offsets, codes_w, scales_w, fmt, out_dtype, ts_a, ts_w, act, out, stream):
     if stream is not None:
-        return _mx_on(fn, stream, codes_a.device, lambda: _mx_product(fn, call, codes_a, scales_a, offsets, codes_w, scales_w, fmt, out_dtype,
-                                                                      ts_a, ts_w, act, out, None))
-    T, K2 = shape = _mx_matrix(fn, "codes_a", codes_a)
-    dev, K = codes_a.device, 2 * K2
-    E, f, a = _mx_groups(fn, offsets, dev), _fmt(fmt), _mx_act(fn, act)
-    block = _mx_block(f)
-    _mx_shape(fn, "codes_a", codes_a, shape, torch.uint8, dev)
-    _mx_shape(fn, "scales_a", scales_a, _mx_tiles(T, K, block, E), torch.uint8, dev)
-    if ts_a is not None:
-        _mx_shape(fn, "ts_a", ts_a, (1,), torch.float32, dev)
-    N = _mx_weights(fn, codes_w, scales_w, E, K, block, dev, ts_w)
-    out = _mx_out(fn, out, T, N, a, out_dtype, dev, E)
-    groups = (offsets.data_ptr(), E) if E else ()
-    _mx_call(fn, call, dev, codes_a.data_ptr(), scales_a.data_ptr(), _mx_ptr(ts_a), T, *groups, codes_w.data_ptr(), scales_w.data_ptr(),
-             _mx_ptr(ts_w), f, N, K, a, out.data_ptr(), _DT.get(out.dtype, -1))
+        return _mx_on(fn, stream, codes_a, lambda: _mx_product(fn, call, codes_a, scales_a, offsets, codes_w, scales_w, fmt, out_dtype, ts_a,
+                                                               ts_w, act, out, None))
+    (T, K2), dev = _mx_first(fn, "codes_a", codes_a, 2)
+    if codes_a.dtype is not _U8:
+        _mx_bad(fn, "codes_a", codes_a, (T, K2), _U8, dev)
+    f, block = _mx_format(fn, fmt)
+    op, E = (None, 0) if offsets is None else _mx_groups(fn, offsets, dev)
+    a = _mx_act(fn, act) if act else 0
+    sa = _mx_ptr(fn, "scales_a", scales_a, (T // 128 + E if E else (T + 127) // 128, (2 * K2 + 4 * block - 1) // (4 * block), 512), _U8, dev)
+    ta = None if ts_a is None else _mx_ptr(fn, "ts_a", ts_a, (1,), _F32, dev)
+    tw = None if ts_w is None else _mx_ptr(fn, "ts_w", ts_w, (E or 1,), _F32, dev)
+    N, cw, sw = _mx_weights(fn, codes_w, scales_w, E, K2, block, dev)
+    out = _mx_out(fn, out, T, N // 2 if a else N, out_dtype, codes_a, E, dev)
+    if E:
+        _mx_call(fn, call, dev, codes_a.data_ptr(), sa, ta, T, op, E, cw, sw, tw, f, N, 2 * K2, a, out.data_ptr(), _DT.get(out.dtype, -1))
+    else:
+        _mx_call(fn, call, dev, codes_a.data_ptr(), sa, ta, T, cw, sw, tw, f, N, 2 * K2, a, out.data_ptr(), _DT.get(out.dtype, -1))
     return out
 
 
@@ -601,25 +603,26 @@ def razer_gemm_mx_grouped_workspace_size(T: int, K: int, groups: int) -> int:
 
 def _mx_online(fn, call, X, offsets, codes_w, scales_w, out_dtype, act, out, workspace, stream):
     if stream is not None:
-        return _mx_on(fn, stream, X.device, lambda: _mx_online(fn, call, X, offsets, codes_w, scales_w, out_dtype, act, out, workspace, None))
-    T, K = _mx_matrix(fn, "X", X)
-    dev = X.device
-    E = 0 if offsets is None else _mx_groups(fn, offsets, dev)
+        return _mx_on(fn, stream, X, lambda: _mx_online(fn, call, X, offsets, codes_w, scales_w, out_dtype, act, out, workspace, None))
+    (T, K), dev = _mx_first(fn, "X", X, 2)
+    op, E = (None, 0) if offsets is None else _mx_groups(fn, offsets, dev)
     a = _mx_act(fn, act) if act else 0
-    N = _mx_weights(fn, codes_w, scales_w, E, K, 32, dev)
-    out = _mx_out(fn, out, T, N, a, out_dtype, dev, E)
+    N, cw, sw = _mx_weights(fn, codes_w, scales_w, E, K // 2, 32, dev)
+    out = _mx_out(fn, out, T, N // 2 if a else N, out_dtype, X, E, dev)
     if workspace is None:
         ws, wp = razer_gemm_mx_grouped_workspace_size(T, K, E), None
         if ws:
-            workspace = torch.empty(ws, dtype=_U8, device=dev)
+            workspace = torch.empty(ws, dtype=_U8, device=X.device)
             wp = workspace.data_ptr()
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"{fn}: workspace must be a contiguous tensor on {dev}")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be a contiguous tensor on {X.device}")
     else:
         ws, wp = workspace.numel() * workspace.element_size(), workspace.data_ptr()
-    groups = (offsets.data_ptr(), E) if E else ()
-    _mx_call(fn, call, dev, X.data_ptr(), _DT.get(X.dtype, -1), T, *groups, codes_w.data_ptr(), scales_w.data_ptr(), N, K, a,
-             out.data_ptr(), _DT.get(out.dtype, -1), wp, ws)
+    dt = _DT.get(X.dtype, -1)
+    if E:
+        _mx_call(fn, call, dev, X.data_ptr(), dt, T, op, E, cw, sw, N, K, a, out.data_ptr(), _DT.get(out.dtype, -1), wp, ws)
+    else:
+        _mx_call(fn, call, dev, X.data_ptr(), dt, T, cw, sw, N, K, a, out.data_ptr(), _DT.get(out.dtype, -1), wp, ws)
     return out
 
 
