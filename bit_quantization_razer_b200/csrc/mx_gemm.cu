@@ -111,15 +111,15 @@ __device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t ad, uint64_t bd, u
 #undef RAZER_MX_MMA
 
 // arrives on `bar` once the MMAs and copies issued so far are done (PAIR: on
-// the barrier at this offset in both CTAs)
+// the barrier at this offset in both CTAs, `mask` of the cluster's ranks)
 template <bool PAIR>
-__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar)
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar, uint16_t mask = 0)
 {
     if constexpr (PAIR)
         asm volatile(
             "{ .reg .pred e; setp.ne.b32 e, %2, 0;\n"
             "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1; }" ::"r"(bar),
-            "h"((uint16_t)3), "r"(lead)
+            "h"(mask), "r"(lead)
             : "memory");
     else
         asm volatile("{ .reg .pred e; setp.ne.b32 e, %1, 0;\n"
@@ -371,6 +371,34 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr)
     return v;
 }
 
+// Adds the sums that the CTAs of a cluster left in their shared memory (column c
+// of lane r at (c * 128 + r) floats from `part`; CTA y of the split is rank
+// rank0 + y * rank_step) and writes the outputs: columns in fours, dealt out
+// over `workers` warps for each quarter of the lanes, added in the CTAs' order.
+// One column at a time took 6 us for 64 columns over two CTAs, a remote load's
+// latency each.
+template <typename TOut, bool GATE>
+__device__ __forceinline__ void join_sums(uint32_t part, int count, int splits, int rank0, int rank_step, int worker, int workers, int q, int n0,
+                                          int N, TOut *__restrict__ Y, int row0, int lane)
+{
+    const int r = q * 32 + lane, n = n0 + r;
+    const int64_t ldy = GATE ? N / 2 : N;
+    for (int c = 4 * worker; c < count; c += 4 * workers) {
+        float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int y = 0; y < splits; y++) {
+            const uint32_t at = cluster_addr(part + (uint32_t)(c * 128 + r) * 4u, (uint32_t)(rank0 + y * rank_step));
+#pragma unroll
+            for (int j = 0; j < 4; j++) a[j] += ld_cluster(at + j * 512);  // past the last column: not written
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            if constexpr (GATE) a[j] = silu_mul<TOut>(a[j], __shfl_xor_sync(0xffffffffu, a[j], 1));
+            if (c + j < count && n < N && !(GATE && (lane & 1))) store1<TOut>(Y + (int64_t)(row0 + c + j) * ldy + (GATE ? n / 2 : n), a[j]);
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // mx_stream_kernel: few rows per group.  A unit is 128 weight rows x up to 64
 // activation rows; its time is the weights' way from HBM, so what matters is
@@ -405,7 +433,7 @@ template <bool NV> struct StreamCfg {
     static_assert(kStreamRing / (kA + kBox + 2 * kS) <= kStreamMaxStages, "barriers for every stage");
     static_assert(kStreamRing / (kA + kStreamRows * 128 + 2 * kS) >= 3, "a ring for the widest unit");
 };
-static_assert(kStreamRows * 128 * 4 <= kStreamRing, "the sums of a cluster's CTA");
+static_assert((kStreamRows + 3) * 128 * 4 <= kStreamRing, "the sums of a cluster's CTA");
 // kFuseRows: up to so many rows a group, on average, an online call quantizes
 // in the product.  Two launches / one, us: 14336 x 4096, 8 rows 10.7 / 9.2, 16
 // rows 10.9 / 10.8, 24 rows 11.2 / 14.2; 28672 x 8192 24.8 / 24.2, 25.0 / 24.8,
@@ -639,19 +667,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             RowWalk walk;
             walk.begin(p, kStreamRows);
             const RowUnit w = walk.at(p, block / ntiles, kStreamRows);
-            const int v = warp - 2, q = v & 3, n = block % ntiles * 128 + q * 32 + lane;
-            const int64_t ldy = GATE ? p.N / 2 : p.N;
-            for (int c = z * 2 + (v >> 2); c < w.count; c += 2 * splits) {
-                const uint32_t at = smem_addr(smem) + (uint32_t)(c * 128 + q * 32 + lane) * 4u;
-                float a = 0.0f;
-                for (int y = 0; y < splits; y++) a += ld_cluster(cluster_addr(at, (uint32_t)y));
-                if constexpr (GATE) {
-                    const float up = __shfl_xor_sync(0xffffffffu, a, 1);
-                    if (n < p.N && !(lane & 1)) store1<TOut>(Y + (int64_t)(w.row0 + c) * ldy + n / 2, silu_mul<TOut>(a, up));
-                } else {
-                    if (n < p.N) store1<TOut>(Y + (int64_t)(w.row0 + c) * ldy + n, a);
-                }
-            }
+            const int v = warp - 2;
+            join_sums<TOut, GATE>(smem_addr(smem), w.count, splits, 0, 1, 2 * z + (v >> 2), 2 * splits, v & 3, block % ntiles * 128, p.N, Y, w.row0,
+                                  lane);
         }
         __syncwarp();
         cluster_sync();  // no CTA leaves while another reads its sums
@@ -677,6 +695,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 //   warp 1: tensor memory, and in the leader the MMA issuer;
 //   warps 2-13: epilogue, three warps per quarter of the lanes: with two the
 //   last unit's, which nothing hides, took 5,300 cycles.
+// Where the units do not fill the pairs, a cluster of 2 or 4 pairs shares one
+// along K, its sums joined as in mx_stream_kernel.
 // Two accumulators of 192 columns: the epilogue of a unit runs beside the MMAs
 // of the next.  384 + 24 (NVFP4: 48) columns of scales fit in 512; 256-wide
 // accumulators would leave no room for them.
@@ -708,6 +728,7 @@ template <bool NV> struct PairCfg {
     static constexpr uint32_t kSfaCols = kStepTiles<NV> * 4, kSfbCols = kStepTiles<NV> * 8;
     static_assert(2 * kPairRows + kSfaCols + kSfbCols <= 512, "tensor memory");
     static_assert(16 * kStages + 40 <= 256, "barriers");
+    static_assert((kPairRows + 3) * 128 * 4 <= kStages * kStage, "the sums of a cluster's CTA");
 };
 
 // An arrival on a barrier of either CTA that orders no memory: it says that
@@ -735,11 +756,11 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
 }
 
 template <bool NV, typename TOut, bool GATE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a,
                    const __grid_constant__ CUtensorMap tmap_a64, const __grid_constant__ CUtensorMap tmap_a32,
                    const __grid_constant__ CUtensorMap tmap_sw, const __grid_constant__ CUtensorMap tmap_sa,
-                   const __grid_constant__ Problem p, PairOrder order, int step, TOut *__restrict__ Y, int inject_stall)
+                   const __grid_constant__ Problem p, PairOrder order, int step, int splits, TOut *__restrict__ Y, int inject_stall)
 {
     using Cfg = PairCfg<NV>;
     constexpr int STAGES = Cfg::kStages;
@@ -751,8 +772,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + 256);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 260);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    // the cluster: `splits` pairs, pair z takes part z of K; `pair` and `pairs` count whole clusters
+    const uint32_t crank = cluster_rank(), rank = crank & 1u, z = crank >> 1, leader = crank & ~1u;
+    const uint16_t both = (uint16_t)(3u << leader);
+    const int pair = blockIdx.x / (2 * splits), pairs = gridDim.x / (2 * splits);
     pdl_trigger();
 
     if (threadIdx.x == 0) {
@@ -779,11 +802,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t tmem = *tmem_slot;
     pdl_wait();  // the activations come from an earlier kernel of the stream
     if (p.E > 0 && blockIdx.x == 0 && warp == 2) check_offsets(p.offsets, p.E, p.T);
-    const int nk = (p.K + kStepK - 1) / kStepK;
+    const int steps = (p.K + kStepK - 1) / kStepK;
+    const int g0 = (int)((int64_t)steps * z / splits), nk = (int)((int64_t)steps * (z + 1) / splits) - g0;  // this pair's stages
 
     if (warp == 0 || warp == kPairEpiWarps + 2) {
         // ---------------- producers ----------------
-        const uint32_t lead = elect_one(), full0 = cluster_addr(full, 0);
+        const uint32_t lead = elect_one(), full0 = cluster_addr(full, leader);
         // the two warps take the stages in turn
         const uint32_t turn = warp == 0 ? 0u : 1u;
         uint32_t s = turn, ph = 0, base = 0;  // base: stages before this unit
@@ -816,11 +840,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 ready = mbar_test(empty + 8 * s, ph ^ 1u);
                 // fault injection (tests only): the first CTA never fills its first stage
                 const bool stall = inject_stall && blockIdx.x == 0 && base == 0 && g == 0;
-                const int t0 = g * kStepTiles<NV> * 2;
+                const int c0 = (g0 + g) * 128, t0 = (g0 + g) * kStepTiles<NV> * 2;
                 if (lead && !stall) {
                     if (rank == 0) mbar_expect_tx(fl, 2 * bytes);
-                    tma_load_2d_pair(a0, &tmap_w, g * 128, wrow, f);
-                    tma_load_2d_pair(a0 + Cfg::kA, tmap_act, g * 128, arow, f);
+                    tma_load_2d_pair(a0, &tmap_w, c0, wrow, f);
+                    tma_load_2d_pair(a0 + Cfg::kA, tmap_act, c0, arow, f);
                     tma_load_3d_pair(s0, &tmap_sw, 0, t0, srow, f);
                     tma_load_3d_pair(s0 + Cfg::kS, &tmap_sa, 0, t0, w.trow, f);
                 }
@@ -866,9 +890,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     ready = mbar_test(full + 8 * s, ph);
                     issue_scales<NV, true, 2>(lead, s0, s0 + Cfg::kS, sfa, sfb);
                     issue_mmas<NV, true, 2>(lead, acc, a0, b0, sfa, sfb, off2, idesc, g == 0);
-                    commit<true>(lead, e);
+                    commit<true>(lead, e, both);
                 }
-                if (ok) commit<true>(lead, acc_full + 8 * b);
+                if (ok) commit<true>(lead, acc_full + 8 * b, both);
             }
             // every MMA issued has completed before the tensor memory is freed (bounded)
             asm volatile("{ .reg .pred e; setp.ne.b32 e, %1, 0; @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(
@@ -883,7 +907,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     } else {
         // ---------------- epilogue ----------------
         const int q = warp & 3, c_first = ((warp - 2) >> 2) * 32;  // quarter of the lanes; which of each 96 columns
-        const uint32_t acc_empty0 = cluster_addr(acc_empty, 0);
+        const uint32_t acc_empty0 = cluster_addr(acc_empty, leader);
         const int64_t ldy = GATE ? p.N / 2 : p.N;
         const float ts_a = p.ts_a ? *p.ts_a : 1.0f;
         uint32_t ti = 0;
@@ -907,14 +931,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8 * b);
                 }
-                write_columns<TOut, GATE>(v, scale, p.N, Y, ldy, w.row0 + c0, w.count - c0, n, lane);
+                if (splits == 1) {
+                    write_columns<TOut, GATE>(v, scale, p.N, Y, ldy, w.row0 + c0, w.count - c0, n, lane);
+                } else {
+                    // the ring is free: the cluster's only unit has been read by its MMAs
+                    float *part = reinterpret_cast<float *>(smem) + c0 * 128 + q * 32 + lane;
+#pragma unroll
+                    for (int i = 0; i < 32; i++)
+                        if (c0 + i < w.count) part[i * 128] = v[i] * scale;
+                }
             }
         }
         tc_fence_before();
     }
     __syncwarp();
     __syncthreads();
-    cluster_sync();  // no CTA leaves while the other may still signal its barriers
+    if (splits > 1) {
+        cluster_sync();  // every CTA's sums are written
+        if (warp >= 2 && warp < kPairEpiWarps + 2) {
+            RowWalk walk;
+            walk.begin(p, step);
+            const RowUnit w = order.rows(walk, p, pair, step);
+            const int v = warp - 2;
+            join_sums<TOut, GATE>(smem_addr(smem), w.count, splits, (int)rank, 2, (kPairEpiWarps / 4) * (int)z + (v >> 2), kPairEpiWarps / 4 * splits,
+                                  v & 3, order.tile(pair) * 256 + (int)rank * 128, p.N, Y, w.row0, lane);
+        }
+        __syncwarp();
+    }
+    cluster_sync();  // no CTA leaves while another may still signal its barriers or read its sums
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
@@ -1023,21 +1067,31 @@ static razer_status launch_stream(const TIn *X, const uint8_t *codes_a, const ui
 
 static int64_t rows_per_group(int64_t T, int64_t E) { return E > 0 ? (T + E - 1) / E : T; }
 
-// Rows of a unit: 192, or fewer where smaller units need no more rounds over
-// the pairs of SMs.  A unit's time goes as 220 + rows (4096 x 4096, one round:
-// 8.7 / 9.6 / 10.4 us for 64 / 128 / 192 rows, 5 of them the launch); so 256
-// rows take 64 at a time (9.2 us, 192 at a time 10.4), 700 rows 192 (11.0;
-// 128: 13.7, 64: 16.8).
-static int pair_step(const Problem &p, int ntiles, int pairs)
+// Rows of a unit (192, or fewer where smaller units need no more rounds over
+// the pairs of SMs) and pairs that share one along K (one unit a cluster then).
+// A stage's time goes as 220 + rows (4096 x 4096, one round of 16 stages: 8.7 /
+// 9.6 / 10.4 us for 64 / 128 / 192 rows, 5 of them the launch), joining the
+// sums takes as long as some 8 stages; so 256 rows take 64 at a time (9.2 us, 192
+// at a time 10.4), 700 rows 192 (11.0; 128: 13.7, 64: 16.8), and 128 rows x 4096 x
+// 14336 take four pairs to a unit (18.0 -> 14.4 us).
+struct PairPlan {
+    int step, splits;
+};
+static PairPlan pair_plan(const Problem &p, int ntiles, const int (&pairs)[3])
 {
-    const int64_t E = p.E ? p.E : 1, rows = rows_per_group(p.T, p.E);
-    int best = kPairRows;
+    const int64_t E = p.E ? p.E : 1, rows = rows_per_group(p.T, p.E), nk = (p.K + kStepK - 1) / kStepK;
+    PairPlan best = {kPairRows, 1};
     int64_t cost = INT64_MAX;
-    for (int step = kPairRows; step >= 64; step -= 64) {
-        const int64_t units = E * ((rows + step - 1) / step) * ntiles, c = (units + pairs - 1) / pairs * (220 + step);
-        if (c < cost) {
-            cost = c;
-            best = step;
+    for (int i = 0; i < (p.E ? 1 : 3); i++) {
+        const int S = 1 << i;
+        for (int step = kPairRows; step >= 64; step -= 64) {
+            const int64_t units = E * ((rows + step - 1) / step) * ntiles;
+            if (S > 1 && (units > pairs[i] || 2 * S > nk)) continue;
+            const int64_t c = (units + pairs[i] - 1) / pairs[i] * ((nk + S - 1) / S + (S > 1 ? 8 : 0)) * (220 + step);
+            if (c < cost) {
+                cost = c;
+                best = {step, S};
+            }
         }
     }
     return best;
@@ -1047,27 +1101,36 @@ template <bool NV, typename TOut, bool GATE>
 static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, TOut *Y, cudaStream_t st)
 {
     using Cfg = PairCfg<NV>;
-    static int resident[64] = {0};  // clusters that the device holds at once
-    int dev = 0;
+    static int resident[64][3] = {};  // clusters of 2, 4, 8 CTAs that the device holds at once
+    int dev = 0, pairs[3];
     cudaGetDevice(&dev);
-    int pairs = dev >= 0 && dev < 64 ? resident[dev] : 0;
-    if (pairs == 0) {
-        if (cudaFuncSetAttribute(mx_pair_kernel<NV, TOut, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmem) != cudaSuccess)
+    const bool known = dev >= 0 && dev < 64 && resident[dev][0] > 0;
+    for (int i = 0; i < 3; i++) {
+        if (known) {
+            pairs[i] = resident[dev][i];
+            continue;
+        }
+        if (i == 0 && cudaFuncSetAttribute(mx_pair_kernel<NV, TOut, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmem) != cudaSuccess)
             return RAZER_ERR_CUDA;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(sm_count() & ~1));
+        cfg.gridDim = dim3((unsigned)(sm_count() / (2 << i) * (2 << i)));
         cfg.blockDim = dim3(kPairThreads);
         cfg.dynamicSmemBytes = Cfg::kSmem;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.x = 2u << i;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&pairs, mx_pair_kernel<NV, TOut, GATE>, &cfg) != cudaSuccess || pairs < 1) return RAZER_ERR_CUDA;
-        pairs = std::min(pairs, sm_count() / 2);
-        if (dev >= 0 && dev < 64) resident[dev] = pairs;
+        if (cudaOccupancyMaxActiveClusters(&pairs[i], mx_pair_kernel<NV, TOut, GATE>, &cfg) != cudaSuccess || pairs[i] < 1) {
+            if (i == 0) return RAZER_ERR_CUDA;
+            (void)cudaGetLastError();
+            pairs[i] = 0;  // a partition that holds none: K is not split so far
+        }
+        pairs[i] = std::min(pairs[i], sm_count() / (2 << i));
     }
+    if (!known && dev >= 0 && dev < 64)
+        for (int i = 2; i >= 0; i--) resident[dev][i] = pairs[i];
     CUtensorMap mw, ma, ma64, ma32, msw, msa;
     const int64_t E = p.E ? p.E : 1, arows = p.E ? tile_rows_grouped(p.T, p.E) : tile_rows(p.T);
     if (!encode_codes_map(&mw, codes_w, p.N * E, p.K, 128) || !encode_codes_map(&ma, codes_a, p.T, p.K, kPairRows / 2) ||
@@ -1075,13 +1138,28 @@ static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, 
         !encode_tiles_map(&msw, p.tiles_w, E * p.trows_w, p.ct, 1, kStepTiles<NV>) ||
         !encode_tiles_map(&msa, p.tiles_a, arows, p.ct, 2, kStepTiles<NV>))
         return RAZER_ERR_CUDA;
-    const int ntiles = (p.N + 255) / 256, step = pair_step(p, ntiles, pairs);
-    const int64_t pieces = max_pieces(p.T, p.E, step), units = pieces * ntiles;
+    const int ntiles = (p.N + 255) / 256;
+    const PairPlan plan = pair_plan(p, ntiles, pairs);
+    const int64_t pieces = max_pieces(p.T, p.E, plan.step), units = pieces * ntiles;
     if (units > INT32_MAX - 1024) return RAZER_ERR_SHAPE;
     const PairOrder order = {ntiles, p.E == 0 && p.T < p.N ? (int)pieces : 0};
     const int inject = fault_injection_enabled() ? 1 : 0;
-    if (launch_pdl(mx_pair_kernel<NV, TOut, GATE>, 2u * (unsigned)std::min<int64_t>(units, pairs), (unsigned)kPairThreads, (size_t)Cfg::kSmem, st, mw,
-                   ma, ma64, ma32, msw, msa, p, order, step, Y, inject) != cudaSuccess)
+    const int64_t clusters = plan.splits > 1 ? units : std::min<int64_t>(units, pairs[0]);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2u * (unsigned)plan.splits * (unsigned)clusters);
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = Cfg::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2u * (unsigned)plan.splits;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, mx_pair_kernel<NV, TOut, GATE>, mw, ma, ma64, ma32, msw, msa, p, order, plan.step, plan.splits, Y, inject) !=
+        cudaSuccess)
         return RAZER_ERR_CUDA;
     return RAZER_OK;
 }
