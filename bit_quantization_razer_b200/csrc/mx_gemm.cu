@@ -419,7 +419,7 @@ __device__ __forceinline__ void join_sums(uint32_t part, int count, int splits, 
 // order (deterministic; no workspace, no second launch).
 // ---------------------------------------------------------------------------
 constexpr int kStreamWorkers = 8, kStreamThreads = 64 + 32 * kStreamWorkers;
-constexpr int kStreamRows = 64, kBoxRows = 32, kFuseRows = 16;
+constexpr int kStreamRows = 64, kBoxRows = 32, kFuseRows = 16, kFuseGroupRows = 4;
 // two CTAs per SM: 227 KB / 2 less 1 KB each that the system keeps
 constexpr uint32_t kStreamRing = 115200u - 1024u - 512u, kStreamSmem = kStreamRing + 512u + 1024u;
 constexpr int kStreamMaxStages = 8;
@@ -437,7 +437,11 @@ static_assert((kStreamRows + 3) * 128 * 4 <= kStreamRing, "the sums of a cluster
 // kFuseRows: up to so many rows a group, on average, an online call quantizes
 // in the product.  Two launches / one, us: 14336 x 4096, 8 rows 10.7 / 9.2, 16
 // rows 10.9 / 10.8, 24 rows 11.2 / 14.2; 28672 x 8192 24.8 / 24.2, 25.0 / 24.8,
-// 25.2 / 33.3: every CTA quantizes all of its rows again.
+// 25.2 / 33.3: every CTA quantizes all of its rows again.  kFuseGroupRows: the
+// same for row groups, whose longest decides.  Random groups, two launches /
+// one: 32 of 2048 x 4096, 4 rows 28.6 / 28.8, 8 rows 30.2 / 38.7; 43 of 466 x
+// 13344, 4 rows 53.7 / 45.1, 8 rows 72 / 114; 64 of 512 x 2048, 6 rows 11.4 /
+// 11.1, 16 rows 12.4 / 15.9.
 
 template <bool NV, typename TOut, bool GATE, typename TIn>
 __global__ void __launch_bounds__(kStreamThreads, 2)
@@ -1200,7 +1204,7 @@ static razer_status run_mx_t(bool nv, const void *X, razer_dtype x_dt, const uin
 }  // namespace mx
 
 // whether an online call quantizes inside the product (few rows per group)
-bool gemm_mx_fuses(int64_t T, int64_t E) { return mx::rows_per_group(T, E) <= mx::kFuseRows; }
+bool gemm_mx_fuses(int64_t T, int64_t E) { return mx::rows_per_group(T, E) <= (E > 0 ? mx::kFuseGroupRows : mx::kFuseRows); }
 
 // E = 0: dense (offsets ignored); otherwise W is [E, N, K] and ts_w holds E
 // scales.  X: the activations, to be quantized to MXFP4 inside the product

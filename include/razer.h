@@ -555,7 +555,7 @@ razer_status razer_gemm_mx_grouped(const uint8_t *codes_a, const uint8_t *scales
  *   workspace  razer_workspace_size(RAZER_OP_GEMM_MX_ONLINE, M, N, K) or
  *              razer_gemm_mx_grouped_workspace_size(T, K, E) bytes (16-byte
  *              aligned; contents on entry ignored): the packed activations.  0
- *              bytes (NULL) for up to 16 rows, or 16 per group on average: the
+ *              bytes (NULL) for up to 16 rows, or 4 per group on average: the
  *              product's kernel then quantizes them itself, in one launch.
  *              Calls that may overlap on the GPU (two streams, two graphs)
  *              need a workspace each.

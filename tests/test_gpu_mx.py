@@ -197,17 +197,18 @@ def test_product_grouped_many_rows_a_group(counts):
         ref.check(y[off[e]:off[e + 1]], r, bound)
 
 
-@pytest.mark.parametrize("counts", [[150] + [0] * 19, [1, 0, 130, 0, 0, 3, 65, 2] + [0] * 12, [7] * 64])
+@pytest.mark.parametrize("counts", [[150] + [0] * 19, [1, 0, 130, 0, 0, 3, 65, 2] + [0] * 12, [7] * 64, [150] + [0] * 37, [1, 0, 130, 0, 0, 3, 65, 2] + [0] * 43,
+                                    [2] * 64, [70, 40, 17, 31, 0, 1] + [0] * 40])
 @pytest.mark.parametrize("gate", [False, True])
 def test_grouped_online_uneven_groups(counts, gate):
-    # few rows a group on average: quantized inside the product, groups of more than one piece among them
+    # few rows a group on average, quantized before the product and (up to 4) inside it, groups of more than one piece among them
     E, N, K, off = len(counts), 96, 544, offsets_of(counts, 1)
     T = off[-1] + 2
     x = dev(matrix(T, K, torch.bfloat16, T, 0.5))
     c, s = ref.random_packed(E * N, K, "mxfp4", E, spread=2)
     cw, sw = dev(c).view(E, N, K // 2), torch.stack([dev(ref.tile(v)) for v in s.reshape(E, N, -1)])
     o = torch.tensor(off, dtype=torch.int32, device=DEV)
-    assert R.razer_gemm_mx_grouped_workspace_size(T, K, E) == 0
+    assert (R.razer_gemm_mx_grouped_workspace_size(T, K, E) == 0) == (T <= 4 * E)
     act = "silu_mul" if gate else None
     codes, tiles = R.razer_quantize_mx(x, o)
     y, z = (torch.full((T, N // 2 if gate else N), 77.0, device=DEV) for _ in range(2))

@@ -72,7 +72,7 @@ def test_sizes(lib):
     assert R.razer_gemm_mx_grouped_workspace_size(0, 160, 7) == 0
     # few rows are quantized inside the product
     assert R.razer_workspace_size(R.RAZER_OP_GEMM_MX_ONLINE, 16, 64, 160) == 0 < R.razer_workspace_size(R.RAZER_OP_GEMM_MX_ONLINE, 17, 64, 160)
-    assert R.razer_gemm_mx_grouped_workspace_size(7 * 16, 160, 7) == 0 < R.razer_gemm_mx_grouped_workspace_size(7 * 16 + 1, 160, 7)
+    assert R.razer_gemm_mx_grouped_workspace_size(7 * 4, 160, 7) == 0 < R.razer_gemm_mx_grouped_workspace_size(7 * 4 + 1, 160, 7)
 
 
 def test_quantizer_refusals(lib):
