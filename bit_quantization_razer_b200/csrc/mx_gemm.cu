@@ -268,6 +268,16 @@ struct RowWalk {
     }
 };
 
+// a * scale and b * scale rounded to a word of 16-bit outputs, a in the low half
+template <typename TOut> __device__ __forceinline__ unsigned pack_scaled(float a, float b, float scale)
+{
+    float x, y;
+    asm("{ .reg .b64 p, s; mov.b64 p, {%2, %3}; mov.b64 s, {%4, %4}; mul.rn.f32x2 p, p, s; mov.b64 {%0, %1}, p; }"
+        : "=f"(x), "=f"(y)
+        : "f"(a), "f"(b), "f"(scale));
+    return Out16<TOut>::pack(x, y);
+}
+
 // two adjacent 16-bit outputs (4-byte aligned)
 template <typename TOut> __device__ __forceinline__ void store_pair(TOut *p, float a, float b)
 {
@@ -279,11 +289,14 @@ template <typename TOut> __device__ __forceinline__ void store_pair(TOut *p, flo
 // two columns, so that the even lane finishes the first row and the odd lane
 // the second: a gated pair meets in one lane and every lane computes one, and
 // 16-bit outputs leave in pairs, 16 stores instead of 32; gated ones swap once
-// more between lanes two apart, 8 stores.  ALL: 32 rows; the chains are then
+// more between lanes two apart, 8 stores.  Outputs without a gate are rounded
+// first, so that one shuffle swaps both rows (4096 x 14336 x 512: 38.4 -> 33.5
+// us).  ALL: 32 rows; the chains are then
 // free of branches and run into each other (with a test between them a unit of
 // 192 rows took 7,000 cycles, longer than its 16 stages of MMAs; with one store
-// per column and lane and the gate tested inside the loop 15,700; now 3,500,
-// gated 4,700).  PAIRS: rows of an even length, so that pairs are 4-byte
+// per column and lane and the gate tested inside the loop 15,700; now 3,100,
+// gated 3,700).  Through shared memory, to leave it as whole lines: 46 us in
+// place of 33.5, two barriers for every 8 rows.  PAIRS: rows of an even length, so that pairs are 4-byte
 // aligned.
 template <typename TOut, bool GATE, bool ALL, bool PAIRS>
 __device__ __forceinline__ void write_columns_n(const float (&v)[32], float scale, TOut *__restrict__ Y, int64_t ldy, int count, bool mine, int n,
@@ -307,19 +320,26 @@ __device__ __forceinline__ void write_columns_n(const float (&v)[32], float scal
             if (mine && (ALL || i + odd + 2 * high < count)) store_pair<TOut>(y, high ? got : r[0], high ? r[1] : got);
             y += 4 * ldy;
         }
-    } else if constexpr (GATE || (sizeof(TOut) == 2 && PAIRS)) {
+    } else if constexpr (sizeof(TOut) == 2 && PAIRS) {
+        // two rows a step, rounded before they are swapped: one shuffle for both
+        TOut *y = Y + odd * ldy + (n & ~1);
+        const unsigned halves = odd ? 0x3276u : 0x5410u;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            if (!ALL && i >= count) break;
+            const unsigned keep = pack_scaled<TOut>(v[i], v[i + 1], scale), got = __shfl_xor_sync(0xffffffffu, keep, 1);
+            if (mine && (ALL || i + odd < count)) *reinterpret_cast<unsigned *>(y) = __byte_perm(keep, got, halves);
+            y += 2 * ldy;
+        }
+    } else if constexpr (GATE) {
         // two rows a step
-        TOut *y = Y + odd * ldy + (GATE ? n / 2 : n & ~1);
+        TOut *y = Y + odd * ldy + n / 2;
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
             if (!ALL && i >= count) break;
             const float keep = (odd ? v[i + 1] : v[i]) * scale, give = (odd ? v[i] : v[i + 1]) * scale;
             const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-            const float even = odd ? got : keep, next = odd ? keep : got;  // columns n & ~1 and n | 1
-            if (mine && (ALL || i + odd < count)) {
-                if constexpr (GATE) store1<TOut>(y, silu_mul<TOut>(even, next));
-                else store_pair<TOut>(y, even, next);
-            }
+            if (mine && (ALL || i + odd < count)) store1<TOut>(y, silu_mul<TOut>(odd ? got : keep, odd ? keep : got));
             y += 2 * ldy;
         }
     } else {
