@@ -1027,18 +1027,26 @@ static bool encode_tiles_map(CUtensorMap *map, const void *base, int64_t trows, 
 // pieces of `step` rows that T rows in E groups can make
 static int64_t max_pieces(int64_t T, int64_t E, int64_t step) { return E == 0 ? (T + step - 1) / step : T / step + (E < T ? E : T); }
 
-// CTAs that share one unit along K: the power of two up to 8 that leaves the
-// busiest SM least to do (units * S CTAs, dealt out over the SMs, 1 / S of a
-// unit each; two stages at least; all of them resident), the smaller on a tie,
-// since joining the sums costs about 0.5 us.  MXFP4, packed, one row: 32 units of K = 4096 in 7.3 /
-// 6.3 / 5.8 / 6.5 us for S = 1 / 2 / 4 / 8; 112 units 9.2 / 9.2 / 13 / 21.
+// CTAs that share one unit along K, 1 to 8 of two stages at least: doubled
+// while the CTAs have an SM each.  (8 rows, us for 1 / 2 / 4 / 8: 16 units of 32
+// stages 13.3 / 9.9 / 7.8 / 7.3, 31 units 13.4 / 10.0 / 8.3 / 8.7.)  Two CTAs to an
+// SM gain from two to four (60 units of 56 stages 21.5 / 15.0 / 14.0), as long as
+// the clusters fit at once (74 units: 15.9 / 24.1); from one to two they gain
+// where the units leave bandwidth over, the longer K the more (80 units: 8.8 / 8.8
+// of 16 stages, 14.1 / 12.4 of 32; 112 units 14.5 / 15.4 of 32, 22.7 / 21.5 of 56);
+// from four to eight nothing.
 static int stream_splits(int64_t units, int64_t steps)
 {
     const int64_t sms = sm_count();
-    int best = 1;
-    for (int S = 2; S <= 8 && 2 * S <= steps && units * S <= 2 * sms; S *= 2)
-        if ((units * S + sms - 1) / sms * best < (units * best + sms - 1) / sms * S) best = S;
-    return best;
+    int S = 1;
+    for (; S < 8 && 4 * S <= steps; S *= 2) {
+        const int64_t ctas = units * 2 * S;
+        if (ctas <= sms) continue;
+        if (S == 1 && ctas <= 2 * sms && units <= 2 * sms / 5 + steps) continue;
+        if (S == 2 && ctas <= 2 * sms - sms / 6) continue;
+        break;
+    }
+    return S;
 }
 
 template <bool NV, typename TOut, bool GATE, typename TIn>

@@ -160,6 +160,18 @@ def test_product(M, N, K, fmt):
     assert R.razer_get_device_status() == 0
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 5700, 2048), (34, 5762, 2080), (2, 9590, 4096)])
+def test_product_split_with_two_blocks_a_processor(M, N, K):
+    # clusters that share a unit along K, more blocks than processors
+    ca, sa, a = packed(M, K, "mxfp4", seed=M)
+    cw, sw, w = packed(N, K, "mxfp4", seed=N)
+    r, _, bound = ref.product(a, w)
+    y = R.razer_gemm_mx(ca, sa, cw, sw, "mxfp4", torch.float32)
+    ref.check(y, r, bound)
+    assert torch.equal(R.razer_gemm_mx(ca, sa, cw, sw, "mxfp4", torch.bfloat16), y.bfloat16())
+    assert R.razer_get_device_status() == 0
+
+
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 @pytest.mark.parametrize("M,N,K", [(1, 128, 256), (5, 34, 96), (40, 256, 320), (130, 514, 512)])
 def test_product_gated(M, N, K, fmt):
