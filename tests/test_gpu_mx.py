@@ -2,6 +2,8 @@
 bit-exact where they write codes, scales or decoded values; the products
 within the bound of fp32 accumulation (mx_reference.product) and half a step
 of the output type."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -476,3 +478,83 @@ def test_first_call_of_a_size_in_a_capture():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, R.razer_gemm_mx(ca, sa, cw, sw, "nvfp4", torch.float16, ts_a=one, ts_w=one, act="silu_mul"))
+
+
+@pytest.mark.parametrize("E", [255, 256, 300])
+def test_hundreds_of_groups(E):
+    # more groups than the quantizer keeps in shared memory
+    N, K = 72, 96
+    counts = [(5 * e) % 4 for e in range(E)]
+    counts[E // 2] = 140
+    off = offsets_of(counts, 1)
+    T = off[-1] + 3
+    x = matrix(T, K, torch.bfloat16, E, 0.0)
+    o = torch.tensor(off, dtype=torch.int32, device=DEV)
+    codes, tiles = R.razer_quantize_mx(dev(x), o)
+    rc, rs = ref.quantize(x.double().numpy())
+    s = slice(off[0], off[-1])
+    assert np.array_equal(ref.unpack(codes.cpu().numpy())[s], rc[s])
+    assert np.array_equal(ref.untile(tiles.cpu().numpy(), T, K // 32, off)[s], rs[s])
+    c, ws = ref.random_packed(E * N, K, "mxfp4", E, spread=2)
+    cw, sw = dev(c).view(E, N, K // 2), torch.stack([dev(ref.tile(v)) for v in ws.reshape(E, N, -1)])
+    y = R.razer_gemm_mx_grouped(codes, tiles, o, cw, sw, out_dtype=torch.float32)
+    assert torch.equal(R.razer_gemm_mx_grouped_online(dev(x), o, cw, sw, torch.float32), y) and not y[0].any() and not y[off[-1]:].any()
+    a, w = ref.values(codes.cpu().numpy(), rs, "mxfp4"), ref.values(c, ws, "mxfp4").reshape(E, N, K)
+    for e in np.flatnonzero(counts):
+        r, _, bound = ref.product(a[off[e]:off[e + 1]], w[e])
+        ref.check(y[off[e]:off[e + 1]], r, bound)
+
+
+def test_calls_of_two_host_threads():
+    N, K = 520, 1024
+    cw, sw, _ = packed(N, K, "mxfp4", 1)
+    xs = [dev(matrix(M, K, torch.bfloat16, M, 0.0)) for M in (3, 200)]
+    want = [R.razer_gemm_mx_online(x, cw, sw) for x in xs]
+    torch.cuda.synchronize()
+    got, failed = [[], []], []
+
+    def calls(i):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(50):
+                got[i].append(R.razer_gemm_mx_online(xs[i], cw, sw, stream=stream))
+            stream.synchronize()
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for i in range(2):
+        assert len(got[i]) == 50 and all(torch.equal(y, want[i]) for y in got[i])
+
+
+def test_captured_grouped_call_with_every_row_in_one_group():
+    # the kernel is chosen by the rows a group on average, at capture; the offsets may then be any
+    E, N, K, T = 40, 136, 288, 400
+    c, ws = ref.random_packed(E * N, K, "mxfp4", E, spread=2)
+    cw, sw = dev(c).view(E, N, K // 2), torch.stack([dev(ref.tile(v)) for v in ws.reshape(E, N, -1)])
+    x = matrix(T, K, torch.bfloat16, T, 0.0)
+    o = torch.tensor([i * 10 for i in range(E + 1)], dtype=torch.int32, device=DEV)
+    xd, y = dev(x), torch.zeros(T, N, device=DEV)
+    R.razer_gemm_mx_grouped_online(xd, o, cw, sw, out=y)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        R.razer_gemm_mx_grouped_online(xd, o, cw, sw, out=y)
+    rc, rs = ref.quantize(x.double().numpy())
+    codes, tiles = R.razer_quantize_mx(xd)
+    a = ref.values(codes.cpu().numpy(), rs, "mxfp4")
+    w = ref.values(c, ws, "mxfp4").reshape(E, N, K)
+    for e in (0, 17, E - 1):
+        o.copy_(torch.tensor([0 if i <= e else T for i in range(E + 1)], dtype=torch.int32))
+        y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        r, _, bound = ref.product(a, w[e])
+        ref.check(y, r, bound)
+    assert R.razer_get_device_status() == 0
