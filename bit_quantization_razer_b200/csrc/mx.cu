@@ -143,7 +143,7 @@ struct RowTiles {
 // would cost the occupancy it is meant to help.  16-byte piece j of lane l's
 // block lies at piece 4 l + (j ^ (l / 2 % 4)), so that eight lanes' reads fall
 // into different banks.
-// Bound: HBM, 2 + 17/32 bytes an element.  14336 x 4096: 25.0 us, 5.96 TB/s
+// Bound: HBM, 2 + 17/32 bytes an element.  14336 x 4096: 25.5 us, 5.8 TB/s
 // (four lanes to a block and direct loads: 34 us).
 constexpr int kQuantizeCtas = 4, kRing = 2;  // CTAs per SM: one wave
 
