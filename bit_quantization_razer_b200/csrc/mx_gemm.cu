@@ -17,6 +17,12 @@
 // Every wait is bounded (~2 s of globaltimer): on expiry the kernel records
 // RAZER_ERR_TIMEOUT, the other roles stop at their next wait, copies in
 // flight are waited for (bounded) and the tensor memory is freed.
+// The allocation of tensor memory has no bound of its own: it waits until the
+// other CTAs of the SM have left enough.  Whoever holds some must therefore be
+// able to end without this CTA.  A programmatic dependent is not: it may have
+// allocated, and then waits in griddepcontrol.wait for this grid.  So the one
+// warp that allocates also lets the dependents in, and only once it has its
+// columns; no other warp may (one thread's trigger counts for its CTA).
 #include <algorithm>
 #include <type_traits>
 
@@ -486,7 +492,6 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     const int g0 = (int)((int64_t)steps * z / splits), nk = (int)((int64_t)steps * (z + 1) / splits) - g0;
     const uint32_t bbytes = (uint32_t)boxes * Cfg::kBox, stage = Cfg::kA + bbytes + 2 * Cfg::kS, stages = kStreamRing / stage;
 
-    pdl_trigger();
     if (warp == 0) {
         // ---------------- producer ----------------
         // It sets up the barriers itself and does not wait for the other warps:
@@ -554,6 +559,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr((const void *)tmem_slot)),
                      "n"(Cfg::kCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        pdl_trigger();  // not before: see the allocation's rule in the header of this file
         tc_fence_before();
         asm volatile("barrier.cta.sync 1, %0;" ::"n"(kStreamThreads) : "memory");
         tc_fence_after();
@@ -800,7 +806,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t crank = cluster_rank(), rank = crank & 1u, z = crank >> 1, leader = crank & ~1u;
     const uint16_t both = (uint16_t)(3u << leader);
     const int pair = blockIdx.x / (2 * splits), pairs = gridDim.x / (2 * splits);
-    pdl_trigger();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; s++) {
@@ -818,6 +823,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr((const void *)tmem_slot)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        pdl_trigger();  // not before: see the allocation's rule in the header of this file
     }
     tc_fence_before();
     __syncthreads();
