@@ -18,7 +18,7 @@ NVCC_FLAGS = [
 
 
 def sources() -> list[str]:
-    srcs = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh"))]
+    srcs = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh", ".h"))]
     return srcs + [os.path.join(INCLUDE, "razer.h")]
 
 

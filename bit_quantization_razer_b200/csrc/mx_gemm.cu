@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "mx.cuh"
+#include "per_device.h"
 #include "sm100_async.cuh"
 #include "sm100_mma.cuh"
 
@@ -1058,14 +1059,15 @@ static int stream_splits(int64_t units, int64_t steps)
 template <bool NV, typename TOut, bool GATE, typename TIn>
 static razer_status launch_stream(const TIn *X, const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, TOut *Y, cudaStream_t st)
 {
-    static bool attr_set[64] = {false};
+    static PerDevice<bool> allowed;
     int dev = 0;
+    bool set;
     cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        if (cudaFuncSetAttribute(mx_stream_kernel<NV, TOut, GATE, TIn>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStreamSmem) != cudaSuccess)
-            return RAZER_ERR_CUDA;
-        if (dev >= 0 && dev < 64) attr_set[dev] = true;
-    }
+    if (!allowed.get(dev, set, [](bool &ok) {
+            return ok = cudaFuncSetAttribute(mx_stream_kernel<NV, TOut, GATE, TIn>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)kStreamSmem) == cudaSuccess;
+        }))
+        return RAZER_ERR_CUDA;
     CUtensorMap mw, ma, msw, msa;
     const int64_t E = p.E ? p.E : 1, arows = p.E ? tile_rows_grouped(p.T, p.E) : tile_rows(p.T);
     if (!encode_codes_map(&mw, codes_w, p.N * E, p.K, 128) || !encode_tiles_map(&msw, p.tiles_w, E * p.trows_w, p.ct, 1, kStepTiles<NV>))
@@ -1115,6 +1117,10 @@ static int64_t rows_per_group(int64_t T, int64_t E) { return E > 0 ? (T + E - 1)
 struct PairPlan {
     int step, splits;
 };
+// clusters of 2, 4, 8 CTAs that the device holds at once
+struct PairClusters {
+    int pairs[3];
+};
 static PairPlan pair_plan(const Problem &p, int ntiles, const int (&pairs)[3])
 {
     const int64_t E = p.E ? p.E : 1, rows = rows_per_group(p.T, p.E), nk = (p.K + kStepK - 1) / kStepK;
@@ -1139,36 +1145,35 @@ template <bool NV, typename TOut, bool GATE>
 static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, TOut *Y, cudaStream_t st)
 {
     using Cfg = PairCfg<NV>;
-    static int resident[64][3] = {};  // clusters of 2, 4, 8 CTAs that the device holds at once
-    int dev = 0, pairs[3];
+    static PerDevice<PairClusters> resident;
+    int dev = 0;
+    PairClusters clusters_of;
     cudaGetDevice(&dev);
-    const bool known = dev >= 0 && dev < 64 && resident[dev][0] > 0;
-    for (int i = 0; i < 3; i++) {
-        if (known) {
-            pairs[i] = resident[dev][i];
-            continue;
-        }
-        if (i == 0 && cudaFuncSetAttribute(mx_pair_kernel<NV, TOut, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmem) != cudaSuccess)
-            return RAZER_ERR_CUDA;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(sm_count() / (2 << i) * (2 << i)));
-        cfg.blockDim = dim3(kPairThreads);
-        cfg.dynamicSmemBytes = Cfg::kSmem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2u << i;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&pairs[i], mx_pair_kernel<NV, TOut, GATE>, &cfg) != cudaSuccess || pairs[i] < 1) {
-            if (i == 0) return RAZER_ERR_CUDA;
-            (void)cudaGetLastError();
-            pairs[i] = 0;  // a partition that holds none: K is not split so far
-        }
-        pairs[i] = std::min(pairs[i], sm_count() / (2 << i));
-    }
-    if (!known && dev >= 0 && dev < 64)
-        for (int i = 2; i >= 0; i--) resident[dev][i] = pairs[i];
+    if (!resident.get(dev, clusters_of, [](PairClusters &c) {
+            if (cudaFuncSetAttribute(mx_pair_kernel<NV, TOut, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmem) != cudaSuccess)
+                return false;
+            for (int i = 0; i < 3; i++) {
+                cudaLaunchConfig_t cfg = {};
+                cfg.gridDim = dim3((unsigned)(sm_count() / (2 << i) * (2 << i)));
+                cfg.blockDim = dim3(kPairThreads);
+                cfg.dynamicSmemBytes = Cfg::kSmem;
+                cudaLaunchAttribute attr[1];
+                attr[0].id = cudaLaunchAttributeClusterDimension;
+                attr[0].val.clusterDim.x = 2u << i;
+                attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+                cfg.attrs = attr;
+                cfg.numAttrs = 1;
+                if (cudaOccupancyMaxActiveClusters(&c.pairs[i], mx_pair_kernel<NV, TOut, GATE>, &cfg) != cudaSuccess || c.pairs[i] < 1) {
+                    if (i == 0) return false;
+                    (void)cudaGetLastError();
+                    c.pairs[i] = 0;  // a partition that holds none: K is not split so far
+                }
+                c.pairs[i] = std::min(c.pairs[i], sm_count() / (2 << i));
+            }
+            return true;
+        }))
+        return RAZER_ERR_CUDA;
+    const int(&pairs)[3] = clusters_of.pairs;
     CUtensorMap mw, ma, ma64, ma32, msw, msa;
     const int64_t E = p.E ? p.E : 1, arows = p.E ? tile_rows_grouped(p.T, p.E) : tile_rows(p.T);
     if (!encode_codes_map(&mw, codes_w, p.N * E, p.K, 128) || !encode_codes_map(&ma, codes_a, p.T, p.K, kPairRows / 2) ||

@@ -1,0 +1,61 @@
+"""The microscaled products as the first calls that a process makes: each test
+runs in an interpreter of its own, where nothing has been set up yet."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+from tests.gpu_helpers import cuda
+
+pytestmark = [pytest.mark.gpu, cuda]
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+HEAD = """
+import threading
+import torch
+import bit_quantization_razer_b200 as R
+from bit_quantization_razer_b200.razer import load
+load()
+g = torch.Generator(device="cuda")
+g.manual_seed(5)
+def packed(rows, K, block=32):
+    codes = torch.randint(0, 256, (rows, K // 2), dtype=torch.uint8, device="cuda", generator=g)
+    fmt = "mxfp4" if block == 32 else "nvfp4"
+    lo, hi = (125, 130) if block == 32 else (40, 80)
+    return codes, torch.randint(lo, hi, R.razer_scale_tiles_shape(rows, K, fmt), dtype=torch.uint8, device="cuda", generator=g)
+"""
+
+
+def run(body):
+    out = subprocess.run([sys.executable, "-c", HEAD + body], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and out.stdout.endswith("ok\n"), out.stdout + out.stderr
+
+
+def test_first_calls_of_host_threads():
+    # K is split over clusters by what the first call finds out: every thread's sums are joined in the same order
+    run("""
+cases = [(3, 200, 8192), (100, 512, 8192), (3, 200, 8192), (100, 512, 8192)]
+args = [(packed(M, K), packed(N, K)) for M, N, K in cases]
+torch.cuda.synchronize()
+got, failed, gate = [[] for _ in cases], [], threading.Barrier(len(cases))
+def calls(i):
+    try:
+        stream = torch.cuda.Stream()
+        gate.wait()
+        for _ in range(5):
+            got[i].append(R.razer_gemm_mx(*args[i][0], *args[i][1], out_dtype=torch.float32, stream=stream))
+        stream.synchronize()
+    except Exception as e:
+        failed.append(e)
+threads = [threading.Thread(target=calls, args=(i,)) for i in range(len(cases))]
+for t in threads: t.start()
+for t in threads: t.join()
+torch.cuda.synchronize()
+assert not failed, failed
+for i in range(len(cases)):
+    want = R.razer_gemm_mx(*args[i][0], *args[i][1], out_dtype=torch.float32)
+    assert len(got[i]) == 5 and all(torch.equal(y, want) for y in got[i]), i
+assert R.razer_get_device_status() == 0
+print("ok")
+""")

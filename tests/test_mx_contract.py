@@ -2,6 +2,7 @@
 CPU: rules whose breach a GPU test could only show by hanging or faulting."""
 import os
 import re
+import subprocess
 
 import pytest
 
@@ -39,3 +40,14 @@ def test_dependents_are_let_in_after_tensor_memory_is_allocated(name):
         assert triggers[0] > alloc, kernel
         between = body[alloc:triggers[0]]
         assert "}" not in between and "else" not in between, kernel  # the warp that allocates
+
+
+def test_tables_of_host_threads(tmp_path):
+    # what a first call finds out is published whole: the thread sanitizer over the table the products keep it in
+    here, exe = os.path.dirname(os.path.abspath(__file__)), str(tmp_path / "per_device_check")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-fsanitize=thread", "-pthread", "-I", CSRC, os.path.join(here, "per_device_check.cpp"), "-o", exe],
+                   check=True)
+    out = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert out.returncode == 0 and "all checks passed" in out.stdout, out.stdout + out.stderr
+    with open(os.path.join(CSRC, "mx_gemm.cu")) as f:
+        assert not re.search(r"static (bool|int) \w+\[", f.read())  # no table of plain values beside it
