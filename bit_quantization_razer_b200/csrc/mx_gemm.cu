@@ -1079,7 +1079,7 @@ static razer_status launch_stream(const TIn *X, const uint8_t *codes_a, const ui
         ma = mw;  // not used
         msa = msw;
     }
-    const int ntiles = (p.N + 127) / 128;
+    const int ntiles = p.trows_w;  // tiles of 128 weight rows; N + 127 may pass 2^31
     const int64_t units = max_pieces(p.T, p.E, kStreamRows) * ntiles;
     if (units > INT32_MAX - 1024) return RAZER_ERR_SHAPE;
     const int S = stream_splits(units, (p.K + kStepK - 1) / kStepK);
@@ -1181,7 +1181,7 @@ static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, 
         !encode_tiles_map(&msw, p.tiles_w, E * p.trows_w, p.ct, 1, kStepTiles<NV>) ||
         !encode_tiles_map(&msa, p.tiles_a, arows, p.ct, 2, kStepTiles<NV>))
         return RAZER_ERR_CUDA;
-    const int ntiles = (p.N + 255) / 256;
+    const int ntiles = (p.trows_w + 1) / 2;
     const PairPlan plan = pair_plan(p, ntiles, pairs);
     const int64_t pieces = max_pieces(p.T, p.E, plan.step), units = pieces * ntiles;
     if (units > INT32_MAX - 1024) return RAZER_ERR_SHAPE;

@@ -51,3 +51,31 @@ def test_quantize_and_product_past_2_31():
     inside = torch.from_numpy(rows[(rows >= 3) & (rows < M - 1)]).to(DEV)
     assert torch.equal(y2[inside], y[inside]) and not y2[:3].any() and not y2[M - 1].any()
     assert torch.equal(y2[M - 200:M - 1], y[M - 200:M - 1])
+
+
+def bytes_of(shape, lo, hi, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return torch.randint(lo, hi, shape, dtype=torch.uint8, device=DEV, generator=g)
+
+
+def test_weight_rows_near_2_31():
+    # the last tile of 128 rows ends at 2^31
+    M, N, K = 2, (1 << 31) - 1, 32
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GB of device memory")
+    cw, sw = bytes_of((N, K // 2), 0, 256, 1), bytes_of(R.razer_scale_tiles_shape(N, K), 120, 135, 2)
+    sw[:, 0].view(-1, 32, 4, 4)[..., 1:] = 0  # what lies past K / 32 = 1 scale
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(3)).to(DEV, torch.bfloat16)
+    ca, sa = R.razer_quantize_mx(x)
+    y = R.razer_gemm_mx(ca, sa, cw, sw)
+    rows = np.unique(np.concatenate([np.arange(200), np.arange(N - 400, N), np.random.default_rng(0).integers(0, N, 200)]))
+    at = torch.from_numpy(rows).to(DEV)
+    w = ref.values(cw[at].cpu().numpy(), sw[at // 128, 0, (at % 32) * 16 + at % 128 // 32 * 4].cpu().numpy()[:, None], "mxfp4")
+    a = ref.values(ca.cpu().numpy(), ref.untile(sa.cpu().numpy(), M, 1), "mxfp4")
+    r, _, bound = ref.product(a, w)
+    ref.check(y[:, at], r, bound)
+    assert R.razer_get_device_status() == 0
+    z = torch.full_like(y, 7.0)
+    R.razer_gemm_mx_online(x, cw, sw, out=z)
+    assert torch.equal(y[0], z[0]) and torch.equal(y[1], z[1])
