@@ -136,6 +136,8 @@ __device__ __forceinline__ void commit(uint32_t lead, uint32_t bar, uint16_t mas
 }
 
 constexpr int kStepK = 256;  // a stage is 128 bytes of codes per row
+// stages of a row of K (K + kStepK may pass 2^31)
+__host__ __device__ constexpr int stages_of(int K) { return K / kStepK + (K % kStepK != 0); }
 template <bool NV> constexpr int kStepTiles = kStepK / (4 * (NV ? 16 : 32));  // scale tiles along a stage: 4 or 2
 
 // The scale copies of one stage: kStepTiles tiles of the weights and of
@@ -488,7 +490,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 260);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int z = splits > 1 ? (int)cluster_rank() : 0, block = blockIdx.x / (unsigned)splits, blocks = gridDim.x / (unsigned)splits;
-    const int steps = (p.K + kStepK - 1) / kStepK;
+    const int steps = stages_of(p.K);
     // this CTA's stages of a unit: g0 .. g0 + nk - 1
     const int g0 = (int)((int64_t)steps * z / splits), nk = (int)((int64_t)steps * (z + 1) / splits) - g0;
     const uint32_t bbytes = (uint32_t)boxes * Cfg::kBox, stage = Cfg::kA + bbytes + 2 * Cfg::kS, stages = kStreamRing / stage;
@@ -618,7 +620,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
                 const int group = (warp - 2) >> 2, tid = (threadIdx.x - 64) & 127;
                 uint4 v[4];
                 auto load = [&](int g, int i) {
-                    const int r = i >> 3, k = (g0 + g) * kStepK + 32 * (i & 7);
+                    const int r = i >> 3;
+                    const int64_t k = (int64_t)(g0 + g) * kStepK + 32 * (i & 7);
                     const bool in = g < nk && i < w.count * 8 && k < p.K;  // past K: zeros
                     const uint4 *x = reinterpret_cast<const uint4 *>(X + (int64_t)(w.row0 + r) * p.K + k);
 #pragma unroll
@@ -833,7 +836,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t tmem = *tmem_slot;
     pdl_wait();  // the activations come from an earlier kernel of the stream
     if (p.E > 0 && blockIdx.x == 0 && warp == 2) check_offsets(p.offsets, p.E, p.T);
-    const int steps = (p.K + kStepK - 1) / kStepK;
+    const int steps = stages_of(p.K);
     const int g0 = (int)((int64_t)steps * z / splits), nk = (int)((int64_t)steps * (z + 1) / splits) - g0;  // this pair's stages
 
     if (warp == 0 || warp == kPairEpiWarps + 2) {
@@ -1082,7 +1085,7 @@ static razer_status launch_stream(const TIn *X, const uint8_t *codes_a, const ui
     const int ntiles = p.trows_w;  // tiles of 128 weight rows; N + 127 may pass 2^31
     const int64_t units = max_pieces(p.T, p.E, kStreamRows) * ntiles;
     if (units > INT32_MAX - 1024) return RAZER_ERR_SHAPE;
-    const int S = stream_splits(units, (p.K + kStepK - 1) / kStepK);
+    const int S = stream_splits(units, stages_of(p.K));
     // one CTA (or cluster) a unit, or where they are more, two CTAs an SM that take several
     const int64_t grid = S > 1 ? units * S : std::min<int64_t>(units, 2 * (int64_t)sm_count());
     const int boxes = p.T <= kBoxRows ? 1 : kStreamRows / kBoxRows;
@@ -1123,7 +1126,7 @@ struct PairClusters {
 };
 static PairPlan pair_plan(const Problem &p, int ntiles, const int (&pairs)[3])
 {
-    const int64_t E = p.E ? p.E : 1, rows = rows_per_group(p.T, p.E), nk = (p.K + kStepK - 1) / kStepK;
+    const int64_t E = p.E ? p.E : 1, rows = rows_per_group(p.T, p.E), nk = stages_of(p.K);
     PairPlan best = {kPairRows, 1};
     int64_t cost = INT64_MAX;
     for (int i = 0; i < (p.E ? 1 : 3); i++) {

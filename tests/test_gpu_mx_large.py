@@ -79,3 +79,38 @@ def test_weight_rows_near_2_31():
     z = torch.full_like(y, 7.0)
     R.razer_gemm_mx_online(x, cw, sw, out=z)
     assert torch.equal(y[0], z[0]) and torch.equal(y[1], z[1])
+
+
+def test_row_length_near_2_31():
+    # few blocks are not zero, the first and the last of a row among them: every sum is exact
+    M, N, K = 2, 3, (1 << 31) - 32
+    if torch.cuda.mem_get_info()[0] < 48 << 30:
+        pytest.skip("needs 48 GB of device memory")
+    C = K // 32
+    blocks = [0, 7, C // 2, C - 9, C - 1]
+    rng = np.random.default_rng(7)
+    ac, wc = (rng.integers(0, 256, (n, len(blocks), 16), dtype=np.uint8) for n in (M, N))
+
+    def matrix(codes):
+        c = torch.zeros(len(codes), K // 2, dtype=torch.uint8, device=DEV)
+        t = torch.full(R.razer_scale_tiles_shape(len(codes), K), 127, dtype=torch.uint8, device=DEV)
+        t[:, -1].view(-1, 32, 4, 4)[..., 3] = 0  # what lies past the last scale
+        for i, b in enumerate(blocks):
+            c[:, 16 * b:16 * b + 16] = torch.from_numpy(codes[:, i]).to(DEV)
+        return c, t
+
+    (ca, sa), (cw, sw) = matrix(ac), matrix(wc)
+    a, w = (ref.E2M1[ref.unpack(v)].reshape(len(v), -1) for v in (ac, wc))
+    want = torch.from_numpy(a @ w.T)  # multiples of 1/4 below 2^13
+    y = R.razer_gemm_mx(ca, sa, cw, sw, out_dtype=torch.float32)
+    assert torch.equal(y.double().cpu(), want)
+    del ca, sa
+    # quantized in the product: a block's largest magnitude 6 or 4 leaves its values as they are
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV)
+    ac[:, :, 0] = 0x77
+    a = ref.E2M1[ref.unpack(ac)].reshape(M, len(blocks), 32)
+    for i, b in enumerate(blocks):
+        x[:, 32 * b:32 * b + 32] = torch.from_numpy(a[:, i]).to(DEV, torch.bfloat16)
+    z = R.razer_gemm_mx_online(x, cw, sw, torch.float32)
+    assert torch.equal(z.double().cpu(), torch.from_numpy(a.reshape(M, -1) @ w.T))
+    assert R.razer_get_device_status() == 0
