@@ -226,6 +226,8 @@ struct RowUnit {
 struct RowWalk {
     int e0, before, start, n, upto, total;  // first group; pieces before it; this lane's group; its pieces' inclusive sum; all 32's
 
+    // ceil(n / step); n + step may pass 2^31
+    static __device__ __forceinline__ int pieces_of(int n, int step) { return n / step + (n % step != 0); }
     __device__ __forceinline__ void load(const Problem &p, int step)
     {
         const int lane = threadIdx.x & 31, e = e0 + lane;
@@ -234,7 +236,7 @@ struct RowWalk {
             start = group_edge(p.offsets, e, p.T);
             n = max(group_edge(p.offsets, e + 1, p.T) - start, 0);
         }
-        upto = (n + step - 1) / step;
+        upto = pieces_of(n, step);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, upto, d);
@@ -267,7 +269,7 @@ struct RowWalk {
         }
         const int src = __ffs(__ballot_sync(0xffffffffu, before + upto > t)) - 1;
         const int s0 = __shfl_sync(0xffffffffu, start, src), sn = __shfl_sync(0xffffffffu, n, src);
-        const int last = before + __shfl_sync(0xffffffffu, upto, src), in = (t - last + (sn + step - 1) / step) * step;
+        const int last = before + __shfl_sync(0xffffffffu, upto, src), in = (t - last + pieces_of(sn, step)) * step;
         u.e = e0 + src;
         u.row0 = s0 + in;
         u.count = min(step, sn - in);
@@ -539,7 +541,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
                     tma_load_2d(a0, &tmap_w, c0, wrow, f);
                     tma_load_3d(s0, &tmap_sw, 0, t0, srow, f);
                     if constexpr (!kFused) {
-                        for (int b = 0; b < boxes; b++) tma_load_2d(a0 + Cfg::kA + b * Cfg::kBox, &tmap_a, c0, w.row0 + b * kBoxRows, f);
+                        // (a box without rows starts behind the unit's last: row0 + kBoxRows may pass 2^31)
+                        for (int b = 0; b < boxes; b++)
+                            tma_load_2d(a0 + Cfg::kA + b * Cfg::kBox, &tmap_a, c0, w.row0 + min(b * kBoxRows, w.count), f);
                         tma_load_3d(s0 + Cfg::kS, &tmap_sa, 0, t0, w.trow, f);
                     }
                 }
@@ -852,7 +856,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const RowUnit w = order.rows(walk, p, u, step);
             if (w.count <= 0) break;
             const int n0 = order.tile(u) * 256 + (int)rank * 128;
-            const int half = ((w.count + 15) & ~15) / 2, arow = w.row0 + (int)rank * half;  // each CTA holds half of the unit's rows
+            const int half = ((w.count + 15) & ~15) / 2, arow = w.row0 + min((int)rank * half, w.count);  // each CTA holds half of the unit's rows
             // the box that holds them, in one copy (three boxes of 32 took a third longer than one of 96)
             const CUtensorMap *tmap_act = half > 64 ? &tmap_a : half > 32 ? &tmap_a64 : &tmap_a32;
             const uint32_t bytes = Cfg::kStage - Cfg::kB + (uint32_t)(half > 64 ? 96 : half > 32 ? 64 : 32) * 128u;

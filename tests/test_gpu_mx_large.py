@@ -59,6 +59,10 @@ def bytes_of(shape, lo, hi, seed):
     return torch.randint(lo, hi, shape, dtype=torch.uint8, device=DEV, generator=g)
 
 
+def dev(a):
+    return torch.from_numpy(a).to(DEV)
+
+
 def test_weight_rows_near_2_31():
     # the last tile of 128 rows ends at 2^31
     M, N, K = 2, (1 << 31) - 1, 32
@@ -114,3 +118,27 @@ def test_row_length_near_2_31():
     z = R.razer_gemm_mx_online(x, cw, sw, torch.float32)
     assert torch.equal(z.double().cpu(), torch.from_numpy(a.reshape(M, -1) @ w.T))
     assert R.razer_get_device_status() == 0
+
+
+def test_a_group_of_2_31_rows():
+    # more rows than 2^31 less a unit of the product: codes of 34 GB, checked at both ends and between
+    T, N, K = (1 << 31) - 1, 2, 32
+    if torch.cuda.mem_get_info()[0] < 72 << 30:
+        pytest.skip("needs 72 GB of device memory")
+    off = [5, T - 1]
+    o = torch.tensor(off, dtype=torch.int32, device=DEV)
+    ca, sa = bytes_of((T, K // 2), 0, 256, 1), bytes_of(R.razer_scale_tiles_shape(T, K, groups=1), 120, 135, 2)
+    sa[:, 0].view(-1, 32, 4, 4)[..., 1:] = 0  # what lies past K / 32 = 1 scale
+    c, s = ref.random_packed(N, K, "mxfp4", 3)
+    y = torch.full((T, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    R.razer_gemm_mx_grouped(ca, sa, o, dev(c)[None], dev(ref.tile(s))[None], out=y)
+    assert R.razer_get_device_status() == 0
+    rows = np.unique(np.concatenate([np.arange(off[0], 400), np.arange(T - 400, off[1]), (1 << 30) + np.arange(-200, 200),
+                                     np.random.default_rng(0).integers(off[0], off[1], 400)]))
+    at = torch.from_numpy(rows).to(DEV)
+    i = at - off[0]
+    scales = sa[i // 128, 0, (i % 32) * 16 + i % 128 // 32 * 4]
+    a = ref.values(ca[at].cpu().numpy(), scales.cpu().numpy()[:, None], "mxfp4")
+    r, _, bound = ref.product(a, ref.values(c, s, "mxfp4"))
+    ref.check(y[at], r, bound)
+    assert (y[:5] == 7).all() and (y[T - 1] == 7).all()
