@@ -223,8 +223,12 @@ struct RowUnit {
 // the groups, for a t that never falls: a warp keeps 32 groups at a time, a
 // lane one of them, and loads the next 32 when t has passed these.  (Reading
 // the offsets again for every unit cost each role some 0.4 us a unit.)
+// The host counts units in the same way (max_pieces): whatever the offsets hold,
+// a call takes no more units than that, and their numbers stay below 2^31.
+// (Offsets that alternate between 0 and T make E / 2 groups of T rows.)
 struct RowWalk {
     int e0, before, start, n, upto, total;  // first group; pieces before it; this lane's group; its pieces' inclusive sum; all 32's
+    int most;  // pieces that T rows in E groups can make: more come of offsets that fall, and are left out
 
     // ceil(n / step); n + step may pass 2^31
     static __device__ __forceinline__ int pieces_of(int n, int step) { return n / step + (n % step != 0); }
@@ -247,7 +251,9 @@ struct RowWalk {
     __device__ __forceinline__ void begin(const Problem &p, int step)
     {
         e0 = before = 0;
-        if (p.E > 0) load(p, step);
+        if (p.E == 0) return;
+        most = p.T / step + min(p.E, p.T);
+        load(p, step);
     }
     // count <= 0: there is no such piece
     __device__ __forceinline__ RowUnit at(const Problem &p, int t, int step)
@@ -261,6 +267,7 @@ struct RowWalk {
             u.off = u.row0 % kTileRows;
             return u;
         }
+        if (t >= most) return u;
         while (t >= before + total) {
             if (e0 + 32 >= p.E) return u;
             before += total;

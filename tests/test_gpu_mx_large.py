@@ -142,3 +142,26 @@ def test_a_group_of_2_31_rows():
     r, _, bound = ref.product(a, ref.values(c, s, "mxfp4"))
     ref.check(y[at], r, bound)
     assert (y[:5] == 7).all() and (y[T - 1] == 7).all()
+
+
+def test_falling_offsets_of_many_groups():
+    # 32768 "groups" of every row: 2^31 units of the product, were they taken as they are.  Nothing
+    # outside the output is written, the work is that of the sizes, and the call is reported
+    T, N, K, E = 1 << 17, 4096, 32, 1 << 16
+    o = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    o[1::2] = T
+    cw, sw = bytes_of((E, N, K // 2), 0, 256, 1), bytes_of((E, N // 128, 1, 512), 120, 135, 2)
+    x = torch.randn(T, K, generator=torch.Generator().manual_seed(3)).to(DEV, torch.bfloat16)
+    guard = 1 << 20
+    room = torch.full((2 * guard + T * N,), 7.0, dtype=torch.bfloat16, device=DEV)
+    y = room[guard:-guard].view(T, N)
+    codes, tiles = R.razer_quantize_mx(x, o)
+    assert R.razer_get_device_status() == 1
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    for call in (lambda: R.razer_gemm_mx_grouped(codes, tiles, o, cw, sw, out=y), lambda: R.razer_gemm_mx_grouped_online(x, o, cw, sw, out=y)):
+        start.record()
+        call()
+        end.record()
+        assert R.razer_get_device_status() == 1
+        assert start.elapsed_time(end) < 2000.0  # 2.2 million units; all of them would take tens of seconds
+        assert (room[:guard] == 7).all() and (room[-guard:] == 7).all()
