@@ -179,17 +179,26 @@ __device__ __forceinline__ void issue_mmas(uint32_t lead, uint32_t acc, uint32_t
 }
 
 // silu(g) * u = g / (1 + exp(-g)) * u.  16-bit outputs take the hardware's
-// 2^x and reciprocal: the exponent's rounding, |g| log2(e) 2^-24, bounds the
-// relative error by 6e-6 where the result is not yet 0 (|g| < 87; below, 2^x
-// passes the range and the reciprocal is 0), against the 2^-9 (2^-12) of the
-// output's own rounding; with expf and an IEEE division the epilogue of 512 x
-// 28672 x 4096 took longer than its MMAs.
+// 2^x and reciprocal.  Both flush what lies below binary32's normal range, so
+// the quotient is formed as (g / 4) / (1/4 + exp(-g) / 4): the reciprocal then
+// stays normal as long as exp(-g) is finite (g > -88.7), and below that is 0, as
+// g / (1 + expf(-g)) is.  (With 1 / (1 + exp(-g)) as it stands, gates between
+// -88.7 and -87.3 gave 0.)  The quarter of g comes with the scale that the sum
+// is multiplied by anyway, kGate in the lanes that hold gates: another multiply
+// here cost 1% (512 x 28672 x 4096 gated 31.8 -> 32.1 us).  Relative error: the
+// exponent -g log2(e), at most 128, is off by 2^-18 of its own rounding and 128 *
+// 2^-26 of the constant's, together 4e-6 of the power; the two functions add
+// 2^-22 each: 5e-6, against the 2^-9 (2^-12) of the output's own rounding.  With
+// expf and an IEEE division the epilogue of 512 x 28672 x 4096 took longer than
+// its MMAs.
+template <typename TOut> constexpr float kGate = sizeof(TOut) == 2 ? 0.25f : 1.0f;
+// g is the gate times kGate
 template <typename TOut> __device__ __forceinline__ float silu_mul(float g, float u)
 {
     if constexpr (sizeof(TOut) == 2) {
         float e, r;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * (4.0f * -1.44269504f)));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, 0.25f, 0.25f)));
         return g * r * u;
     } else {
         return g / (1.0f + expf(-g)) * u;
@@ -321,6 +330,7 @@ __device__ __forceinline__ void write_columns_n(const float (&v)[32], float scal
                                                 int lane)
 {
     const int odd = lane & 1, high = (lane >> 1) & 1;
+    if (GATE && !odd) scale *= kGate<TOut>;  // this lane's sums are gates
     if constexpr (sizeof(TOut) == 2 && GATE && PAIRS) {
         // four rows a step; outputs n / 2 & ~1 and n / 2 | 1
         TOut *y = Y + (odd + 2 * high) * ldy + (n / 2 & ~1);
@@ -431,7 +441,7 @@ __device__ __forceinline__ void join_sums(uint32_t part, int count, int splits, 
         }
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            if constexpr (GATE) a[j] = silu_mul<TOut>(a[j], __shfl_xor_sync(0xffffffffu, a[j], 1));
+            if constexpr (GATE) a[j] = silu_mul<TOut>(a[j] * kGate<TOut>, __shfl_xor_sync(0xffffffffu, a[j], 1));
             if (c + j < count && n < N && !(GATE && (lane & 1))) store1<TOut>(Y + (int64_t)(row0 + c + j) * ldy + (GATE ? n / 2 : n), a[j]);
         }
     }

@@ -514,7 +514,10 @@ razer_status razer_tile_scales(const uint8_t *scales, int64_t batch, int64_t R, 
 /* What a product writes: the sums, or (RAZER_ACT_SILU_MUL) for weights whose
  * row 2j is a gate and row 2j + 1 its up projection, the N / 2 outputs
  * Y[m, j] = silu(g) * u = g / (1 + exp(-g)) * u, with g = sum of row 2j and u
- * = sum of row 2j + 1 in fp32 and one rounding to out_dt. */
+ * = sum of row 2j + 1 in fp32 and one rounding to out_dt.  The quotient is
+ * taken in fp32: it is 0 where exp(-g) passes fp32's range (g < -88.7).  For
+ * 16-bit outputs exp and the division are the hardware's approximations, off
+ * by 5e-6 relative at most; for fp32 outputs expf and an IEEE division. */
 typedef enum { RAZER_ACT_NONE = 0, RAZER_ACT_SILU_MUL = 1 } razer_act;
 
 /*
