@@ -206,12 +206,13 @@ template <typename TOut> __device__ __forceinline__ float silu_mul(float g, floa
 }
 
 // One product: N, K of the weights, T activation rows (in all groups), E = 0:
-// dense.  tiles_w holds trows_w tile rows per expert, ct tiles each.
+// dense.  tiles_w holds trows_w tile rows per expert, ct tiles each.  pieces:
+// how many the rows can make of those that the kernel takes at a time.
 struct Problem {
     const uint8_t *tiles_a, *tiles_w;
     const float *ts_a, *ts_w;  // NULL: 1
     const int32_t *offsets;
-    int E, T, N, K, ct, trows_w, gate;
+    int E, T, N, K, ct, trows_w, gate, pieces;
 };
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar)
@@ -232,12 +233,11 @@ struct RowUnit {
 // the groups, for a t that never falls: a warp keeps 32 groups at a time, a
 // lane one of them, and loads the next 32 when t has passed these.  (Reading
 // the offsets again for every unit cost each role some 0.4 us a unit.)
-// The host counts units in the same way (max_pieces): whatever the offsets hold,
-// a call takes no more units than that, and their numbers stay below 2^31.
-// (Offsets that alternate between 0 and T make E / 2 groups of T rows.)
+// No piece from p.pieces on is taken: whatever the offsets hold, a call has no
+// more units than the host planned, and their numbers stay below 2^31.  (Offsets
+// that alternate between 0 and T make E / 2 groups of T rows.)
 struct RowWalk {
     int e0, before, start, n, upto, total;  // first group; pieces before it; this lane's group; its pieces' inclusive sum; all 32's
-    int most;  // pieces that T rows in E groups can make: more come of offsets that fall, and are left out
 
     // ceil(n / step); n + step may pass 2^31
     static __device__ __forceinline__ int pieces_of(int n, int step) { return n / step + (n % step != 0); }
@@ -260,23 +260,20 @@ struct RowWalk {
     __device__ __forceinline__ void begin(const Problem &p, int step)
     {
         e0 = before = 0;
-        if (p.E == 0) return;
-        most = p.T / step + min(p.E, p.T);
-        load(p, step);
+        if (p.E > 0) load(p, step);
     }
     // count <= 0: there is no such piece
     __device__ __forceinline__ RowUnit at(const Problem &p, int t, int step)
     {
         RowUnit u = {0, 0, 0, 0, 0};
+        if (t >= p.pieces) return u;
         if (p.E == 0) {
-            if ((int64_t)t * step >= p.T) return u;  // 64 bits: T may be near 2^31
             u.row0 = t * step;
             u.count = min(step, p.T - u.row0);
             u.trow = u.row0 / kTileRows;
             u.off = u.row0 % kTileRows;
             return u;
         }
-        if (t >= most) return u;
         while (t >= before + total) {
             if (e0 + 32 >= p.E) return u;
             before += total;
@@ -1081,7 +1078,7 @@ static int stream_splits(int64_t units, int64_t steps)
 }
 
 template <bool NV, typename TOut, bool GATE, typename TIn>
-static razer_status launch_stream(const TIn *X, const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, TOut *Y, cudaStream_t st)
+static razer_status launch_stream(const TIn *X, const uint8_t *codes_a, const uint8_t *codes_w, Problem p, TOut *Y, cudaStream_t st)
 {
     static PerDevice<bool> allowed;
     int dev = 0;
@@ -1104,8 +1101,9 @@ static razer_status launch_stream(const TIn *X, const uint8_t *codes_a, const ui
         msa = msw;
     }
     const int ntiles = p.trows_w;  // tiles of 128 weight rows; N + 127 may pass 2^31
-    const int64_t units = max_pieces(p.T, p.E, kStreamRows) * ntiles;
+    const int64_t pieces = max_pieces(p.T, p.E, kStreamRows), units = pieces * ntiles;
     if (units > INT32_MAX - 1024) return RAZER_ERR_SHAPE;
+    p.pieces = (int)pieces;
     const int S = stream_splits(units, stages_of(p.K));
     // one CTA (or cluster) a unit, or where they are more, two CTAs an SM that take several
     const int64_t grid = S > 1 ? units * S : std::min<int64_t>(units, 2 * (int64_t)sm_count());
@@ -1166,7 +1164,7 @@ static PairPlan pair_plan(const Problem &p, int ntiles, const int (&pairs)[3])
 }
 
 template <bool NV, typename TOut, bool GATE>
-static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, const Problem &p, TOut *Y, cudaStream_t st)
+static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, Problem p, TOut *Y, cudaStream_t st)
 {
     using Cfg = PairCfg<NV>;
     static PerDevice<PairClusters> resident;
@@ -1209,6 +1207,7 @@ static razer_status launch_pair(const uint8_t *codes_a, const uint8_t *codes_w, 
     const PairPlan plan = pair_plan(p, ntiles, pairs);
     const int64_t pieces = max_pieces(p.T, p.E, plan.step), units = pieces * ntiles;
     if (units > INT32_MAX - 1024) return RAZER_ERR_SHAPE;
+    p.pieces = (int)pieces;
     const PairOrder order = {ntiles, p.E == 0 && p.T < p.N ? (int)pieces : 0};
     const int inject = fault_injection_enabled() ? 1 : 0;
     const int64_t clusters = plan.splits > 1 ? units : std::min<int64_t>(units, pairs[0]);
@@ -1291,6 +1290,7 @@ razer_status run_gemm_mx(const void *X, razer_dtype x_dt, const uint8_t *codes_a
     p.ct = (int)mx::tile_cols(nv, K);
     p.trows_w = (int)mx::tile_rows(N);
     p.gate = gate;
+    p.pieces = 0;  // the launch knows
     if (out_dt == RAZER_F32) return mx::run_mx_t<float>(nv, X, x_dt, codes_a, codes_w, p, reinterpret_cast<float *>(Y), st);
     if (out_dt == RAZER_F16) return mx::run_mx_t<__half>(nv, X, x_dt, codes_a, codes_w, p, reinterpret_cast<__half *>(Y), st);
     return mx::run_mx_t<__nv_bfloat16>(nv, X, x_dt, codes_a, codes_w, p, reinterpret_cast<__nv_bfloat16 *>(Y), st);
