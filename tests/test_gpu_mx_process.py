@@ -59,3 +59,40 @@ for i in range(len(cases)):
 assert R.razer_get_device_status() == 0
 print("ok")
 """)
+
+
+@pytest.mark.parametrize("call", [
+    "R.razer_gemm_mx(*packed(3, 4096), *packed(200, 4096), out=few)",
+    "R.razer_gemm_mx(*packed(130, 96, 16), *packed(258, 96, 16), 'nvfp4', ts_a=one, ts_w=one, act='silu_mul', out=out)",
+    "R.razer_gemm_mx_online(x, *packed(256, 96), out=y)",
+])
+def test_first_call_of_a_process_in_a_capture(call):
+    # what a call does for the first time (attributes, occupancy, the driver's entry point) is not barred while capturing
+    run("""
+one = torch.ones(1, device="cuda")
+x = torch.randn(100, 96, device="cuda", generator=g).bfloat16()
+y = torch.zeros(100, 256, device="cuda", dtype=torch.bfloat16)
+out = torch.zeros(130, 129, device="cuda", dtype=torch.float16)
+operands = {}
+real = packed
+def packed(rows, K, block=32):  # made once, before the capture
+    key = (rows, K, block)
+    if key not in operands: operands[key] = real(rows, K, block)
+    return operands[key]
+CALL = lambda: %s
+""" % call + """
+few = torch.zeros(3, 200, device="cuda", dtype=torch.float32)
+for args in ((3, 4096), (200, 4096), (130, 96, 16), (258, 96, 16), (256, 96)): packed(*args)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    result = CALL()
+assert not result.any()  # captured, not run
+graph.replay()
+torch.cuda.synchronize()
+captured = result.clone()
+result.zero_()
+assert captured.any() and torch.equal(CALL(), captured)
+assert R.razer_get_device_status() == 0
+print("ok")
+""")
