@@ -739,8 +739,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 // Bound: a stage of 192 rows takes 401 cycles (MXFP4; NVFP4 415) against the
 // 384 of its MMAs, 390 (398) with the loads left out; of 64 rows 325, the
 // issuing warp's own latency.  4096 x 4096 x 4096 in 28.1 us (4.9 PFLOP/s).
-// Larger calls meet the power limit: 4096 x 14336 x 4096 takes 147,000 cycles,
-// 95 us, at 1.5 GHz.
+// Large calls take more than their stages: 4096 x 14336 x 4096, 17 rounds of 16
+// stages, 147,000 cycles where 17 x 16 x 401 are 109,000 (start and last epilogue
+// 10,000; the rest, 1,600 a unit, is not accounted for), and at the 1000 W limit
+// the clock falls to 1.5 GHz, 95 us.
 //   warps 0 and 14: bulk-tensor producers, a stage in turn (each CTA loads its
 //   own operands; the leader's barrier counts both); one warp alone needs 390
 //   cycles for a stage's four copies, as long as its MMAs take;
